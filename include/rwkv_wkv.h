@@ -227,6 +227,108 @@ int rwkv_wkv6_backward_omega_bf16(int64_t B, int64_t T, int64_t H, int64_t N,
                                   float *dr, float *dk, float *dv, float *domega, float *du,
                                   float *ds0, void *workspace, size_t workspace_bytes);
 
+/* ------------------------------------------------------------------ gated delta rule
+ * The recurrence whose state is corrected towards each new value instead of only decayed:
+ * per sequence and value head h, state S (N x N, row i = key channel, column j = value
+ * channel, as in WKV-6), for each token t:
+ *   S'  = exp(g_t) S                       decay, one factor per token and head
+ *   u_t = beta_t (v_t - k_t S')            what k_t does not recall yet of v_t
+ *   S   = S' + k_t^T u_t
+ *   o_t = scale q_t S                      (reads the state after the token's update)
+ * with S = s0 before the first token and sT = S after the last.
+ *   q, k    : [B, T, Hk, N];   v, o : [B, T, H, N].  Hk divides H; value head h uses key
+ *             head h / (H / Hk).  Queries and keys are used as given (the caller
+ *             normalises them).
+ *   g, beta : [B, T, H], in the type of q: the log of the decay (<= 0 for a decay; -inf
+ *             forgets the state) and the gate of the update.
+ *   scale   : finite (RWKV_ERR_ARG otherwise).
+ *   offsets : NULL: the B rows are the sequences.  Otherwise int32 [nseq + 1] on the device,
+ *             and B must be 1: sequence i is the tokens offsets[i] .. offsets[i+1] - 1 of
+ *             the T packed ones (ascending; a sequence may be empty).  Tokens outside every
+ *             sequence are neither read nor written.  Values outside 0 .. T are clamped.
+ *             nseq is ignored without offsets.
+ *   s0, sT  : fp32, NULL = zero state / not written; sT may equal s0 (in place).  Without
+ *             slots, [nseq, H, N, N].  With slots, a pool [nslots, H, N, N] where sequence i
+ *             uses state slots[i] (int32 [nseq] on the device); the other slots are neither
+ *             read nor written.  A negative slot means no state: the sequence starts from
+ *             zero and its last state is dropped (a padding row of a decode batch).  A slot
+ *             past the pool does the same and records RWKV_ERR_ARG in the device status
+ *             word.  A slot named by two sequences of one call ends with the state of one
+ *             of them, or, in place, of either started from any mix of the two: name each
+ *             slot once (rwkv_state_copy forks states).  nslots is ignored without slots.
+ *   N must be 64.  Index arrays are 4-byte aligned; other rules and errors as above.
+ * Accumulation is fp32 and the state is held in fp32 throughout.
+ */
+int rwkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                       const float *q, const float *k, const float *v, const float *g,
+                       const float *beta, float scale, int64_t nseq, const int32_t *offsets,
+                       int64_t nslots, const int32_t *slots, const float *s0, float *o,
+                       float *sT);
+int rwkv_delta_forward_bf16(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                            const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                            const uint16_t *g, const uint16_t *beta, float scale, int64_t nseq,
+                            const int32_t *offsets, int64_t nslots, const int32_t *slots,
+                            const float *s0, uint16_t *o, float *sT);
+
+/* Backward pass of the gated delta rule.  Given dout = dL/do ([B, T, H, N], type of q) and
+ * dsT = dL/dsT ([nseq, H, N, N] fp32, NULL = 0) it writes, with D the gradient of the state
+ * after token t, r_t = v_t - k_t S' and S the state after token t:
+ *   D += scale q_t^T do_t;   du = k_t D
+ *   dq_t = scale S do_t^T    dv_t = beta_t du         dbeta_t = du . r_t
+ *   dk_t = D u_t^T - S' dv_t^T   (dq and dk summed over the value heads of a key head)
+ *   D' = D - k_t^T dv_t      dg_t = sum_ij D' S'      D <- exp(g_t) D'
+ *   ds0 = D before the first token.
+ *   dq, dk : [B, T, Hk, N];  dv : [B, T, H, N];  dg, dbeta : [B, T, H], in the type of the
+ *            inputs;  ds0 : [nseq, H, N, N] fp32, NULL = not written; may equal dsT.
+ *   Gradients of tokens outside every sequence are not written.
+ *   workspace : device scratch owned by the caller, 16-byte aligned, of at least the bytes
+ *            that rwkv_delta_backward_workspace_bytes reports for the same sizes (packed:
+ *            offsets given; bf16: the entry point's type); fewer are refused with
+ *            RWKV_ERR_ARG.  No initialisation needed, undefined afterwards; calls whose work
+ *            overlaps need a workspace each.
+ * Results are deterministic.  No output may overlap an input, the workspace or another
+ * output (except ds0 == dsT).  Other rules as rwkv_delta_forward. */
+int rwkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                                        int64_t nseq, int packed, int bf16, size_t *bytes);
+int rwkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                        const float *q, const float *k, const float *v, const float *g,
+                        const float *beta, float scale, int64_t nseq, const int32_t *offsets,
+                        const float *s0, const float *dout, const float *dsT, float *dq,
+                        float *dk, float *dv, float *dg, float *dbeta, float *ds0,
+                        void *workspace, size_t workspace_bytes);
+int rwkv_delta_backward_bf16(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                             const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                             const uint16_t *g, const uint16_t *beta, float scale, int64_t nseq,
+                             const int32_t *offsets, const float *s0, const uint16_t *dout,
+                             const float *dsT, uint16_t *dq, uint16_t *dk, uint16_t *dv,
+                             uint16_t *dg, uint16_t *dbeta, float *ds0, void *workspace,
+                             size_t workspace_bytes);
+
+/* ------------------------------------------------------------------ pools of states
+ * A serving process keeps the recurrent states of its sequences in the slots of a pool,
+ * [layers, nslots, slot_bytes], of any of the state layouts above (slot_bytes a multiple of
+ * 16, RWKV_ERR_ALIGN otherwise).
+ *
+ * rwkv_state_copy: for the n pairs (n <= 4096, RWKV_ERR_SHAPE otherwise), in every layer,
+ *   slot dst[i] <- slot src[i] as it was before the call
+ * so that any set of pairs, swaps and shifts included, is one call.  One src in several
+ * pairs forks a state; src[i] < 0 frees dst[i] (zeros it: the empty state of WKV-6 and the
+ * delta rule); dst[i] < 0 leaves the pair out.  Where several pairs name one dst, the last
+ * of them counts.  A pair with an index past the pool is left out and RWKV_ERR_ARG recorded
+ * in the device status word.  src, dst: int32 [n] on the device.
+ *
+ * rwkv_state_compact: moves the live slots (live[i] != 0, one byte each) to the front of the
+ * pool in their order, in every layer: new_index[i] = the number of live slots before slot
+ * i, or -1 if it is not live, and *count = the number of live slots.  The slots from *count
+ * on keep what they hold.  nslots <= 16384 (RWKV_ERR_SHAPE otherwise).  live, new_index
+ * ([nslots] int32) and count (int32) are on the device.
+ *
+ * Both are asynchronous and allocate nothing.  The arrays must not overlap one another. */
+int rwkv_state_copy(int64_t layers, int64_t nslots, int64_t slot_bytes, void *pool, int64_t n,
+                    const int32_t *src, const int32_t *dst);
+int rwkv_state_compact(int64_t layers, int64_t nslots, int64_t slot_bytes, void *pool,
+                       const uint8_t *live, int32_t *new_index, int32_t *count);
+
 /* Kernel choice for WKV-6 on the calling thread: RWKV_WKV6_AUTO (default, as above),
  * RWKV_WKV6_SERIAL (always the serial kernel; the backward takes the exact fp32 walks),
  * RWKV_WKV6_CHUNKED (the chunked kernel for bf16 whatever T; ignored for fp32).  Returns

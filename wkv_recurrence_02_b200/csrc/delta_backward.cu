@@ -1,0 +1,305 @@
+// delta_backward.cu -- gradients of the gated delta rule by exact fp32 walks (CUDA cores).
+//
+// Forward, per sequence and value head (a_t = exp(g_t)):
+//   S' = a_t S,   r_t = v_t - k_t S',   u_t = beta_t r_t,   S = S' + k_t^T u_t,   o_t = scale q_t S.
+// With D the gradient of the state after token t, walked backwards in time:
+//   D += scale q_t^T do_t
+//   dq_t = scale S do_t^T,   du = k_t D,   dbeta_t = du . r_t,   dv_t = beta_t du
+//   dk_t = D u_t^T - S' dv_t^T,   D' = D - k_t^T dv_t,   dg_t = <D', S'>,   D = a_t D'.
+//
+// One block owns one (sequence, value head).  A forward pass leaves the state before every 8th
+// token in the workspace; the backward pass takes 8 tokens at a time, forms their states again
+// from that checkpoint (each thread keeps its own 16 elements of the 8 states in shared memory)
+// and then walks them in reverse.  Warp w owns columns 8 w .. 8 w + 7; lane (rg, cq) rows
+// 8 rg .. 8 rg + 7 of columns 2 cq, 2 cq + 1 of those.  Sums over rows are shuffles; sums over
+// columns (dq, dk, dbeta, dg) leave the block's eight warps through shared memory once per 8
+// tokens, added in a fixed order.  Value heads that share a key head write their shares of dq
+// and dk to the workspace and a second kernel adds them, also in a fixed order.
+//
+// Bound by the chain of one token; the tensor-core path serves bf16.
+#include "wkv_internal.cuh"
+
+namespace wkv {
+namespace {
+
+constexpr int kN = 64;
+constexpr int kThreads = 256;
+constexpr int kSeg = 8;  // tokens between checkpoints
+constexpr int kPart = 2 * kN + 2;  // dq, dk, dbeta, dg of one token
+// shared memory, floats: states [kSeg][4][256][4], r [kSeg][64], partial sums [kSeg][8][kPart]
+constexpr int kSmemBytes = (kSeg * 4096 + kSeg * kN + kSeg * 8 * kPart) * 4;
+
+__device__ __forceinline__ float rd(const float *p) { return *p; }
+__device__ __forceinline__ float rd(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void wr(float *p, float x) { *p = x; }
+__device__ __forceinline__ void wr(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+struct WalkParams {
+    int64_t B, T, Hk, H, nseq;
+    const int32_t *offsets;
+    float scale;
+    const float *s0, *dsT;
+    float *ds0;
+    float *ckpt;        // [checkpoints][H][64][64]
+    float *dq_h, *dk_h; // [B,T,H,64] shares of the value heads, or null (no shared key heads)
+    int64_t nckpt;
+    int *status;
+};
+
+// Checkpoint index of a sequence's first segment: sequences take disjoint runs, since each
+// needs at most one more than its share of the tokens.
+__device__ __forceinline__ int64_t first_segment(int64_t first, int64_t seq) { return first / kSeg + seq; }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                   const T *__restrict__ g, const T *__restrict__ beta, const T *__restrict__ dout,
+                   T *__restrict__ dq, T *__restrict__ dk, T *__restrict__ dv, T *__restrict__ dg,
+                   T *__restrict__ dbeta)
+{
+    extern __shared__ float sm[];
+    float *states = sm, *rs = sm + kSeg * 4096, *part = rs + kSeg * kN;
+    const int64_t n = blockIdx.x, seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = lane >> 2, row = 8 * rg;
+    const int col = 8 * warp + 2 * (lane & 3);
+    int64_t first, len;
+    sequence_span(p.offsets, seq, p.T, &first, &len);
+    const int64_t nseg = (len + kSeg - 1) / kSeg, seg0 = first_segment(first, seq);
+    const int64_t ntok = p.B * p.T;
+    if (!in_bounds(p.status, first, len, ntok) || !in_bounds(p.status, seg0, nseg, p.nckpt)) return;
+
+    float S[8][2], D[8][2];
+    const int64_t base = (seq * p.H + h) * kN * kN;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const float2 x = p.s0 ? *reinterpret_cast<const float2 *>(p.s0 + base + (row + m) * kN + col) : make_float2(0.f, 0.f);
+        S[m][0] = x.x, S[m][1] = x.y;
+    }
+    // one token forward: S becomes the state after it; r (this lane's two columns) is returned
+    auto step = [&](int64_t t, float (&r)[2]) {
+        const int64_t th = t * p.H + h;
+        const T *pk = k + (t * p.Hk + hk) * kN + row;
+        const float a = expf(rd(g + th)), b = rd(beta + th);
+        float kk[8], ks[2] = {};
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            kk[m] = rd(pk + m);
+            ks[0] = fmaf(kk[m], S[m][0], ks[0]);
+            ks[1] = fmaf(kk[m], S[m][1], ks[1]);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) {
+            ks[0] += __shfl_xor_sync(0xffffffffu, ks[0], d);
+            ks[1] += __shfl_xor_sync(0xffffffffu, ks[1], d);
+        }
+        r[0] = rd(v + th * kN + col) - a * ks[0];
+        r[1] = rd(v + th * kN + col + 1) - a * ks[1];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            S[m][0] = fmaf(kk[m], b * r[0], a * S[m][0]);
+            S[m][1] = fmaf(kk[m], b * r[1], a * S[m][1]);
+        }
+    };
+    float r[2];
+    for (int64_t sg = 0; sg < nseg; ++sg) {
+        float *ck = p.ckpt + ((seg0 + sg) * p.H + h) * kN * kN;
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+            *reinterpret_cast<float2 *>(ck + (row + m) * kN + col) = make_float2(S[m][0], S[m][1]);
+        if (sg + 1 < nseg)
+            for (int i = 0; i < kSeg; ++i) step(first + sg * kSeg + i, r);
+    }
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const float2 x = p.dsT ? *reinterpret_cast<const float2 *>(p.dsT + base + (row + m) * kN + col) : make_float2(0.f, 0.f);
+        D[m][0] = x.x, D[m][1] = x.y;
+    }
+    for (int64_t sg = nseg - 1; sg >= 0; --sg) {
+        const int64_t t0 = first + sg * kSeg;
+        const int cnt = static_cast<int>(min(static_cast<int64_t>(kSeg), len - sg * kSeg));
+        const float *ck = p.ckpt + ((seg0 + sg) * p.H + h) * kN * kN;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {  // this thread's own elements, written above
+            const float2 x = *reinterpret_cast<const float2 *>(ck + (row + m) * kN + col);
+            S[m][0] = x.x, S[m][1] = x.y;
+        }
+        for (int i = 0; i < cnt; ++i) {
+            float4 *mine = reinterpret_cast<float4 *>(states) + i * 1024 + tid;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) mine[m * 256] = make_float4(S[2 * m][0], S[2 * m][1], S[2 * m + 1][0], S[2 * m + 1][1]);
+            step(t0 + i, r);
+            if (rg == 0) *reinterpret_cast<float2 *>(rs + i * kN + col) = make_float2(r[0], r[1]);
+        }
+        __syncwarp();
+        for (int i = cnt - 1; i >= 0; --i) {
+            const int64_t t = t0 + i, th = t * p.H + h;
+            const float4 *mine = reinterpret_cast<const float4 *>(states) + i * 1024 + tid;
+            const float a = expf(rd(g + th)), b = rd(beta + th);
+            const T *pk = k + (t * p.Hk + hk) * kN + row, *pq = q + (t * p.Hk + hk) * kN + row;
+            const float d0 = rd(dout + th * kN + col), d1 = rd(dout + th * kN + col + 1);
+            const float2 rr = *reinterpret_cast<const float2 *>(rs + i * kN + col);
+            float kk[8], pdq[8], sp[8][2], du[2] = {};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float4 x = mine[m * 256];
+                sp[2 * m][0] = a * x.x, sp[2 * m][1] = a * x.y, sp[2 * m + 1][0] = a * x.z, sp[2 * m + 1][1] = a * x.w;
+            }
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                kk[m] = rd(pk + m);
+                const float qq = p.scale * rd(pq + m);
+                D[m][0] = fmaf(qq, d0, D[m][0]);
+                D[m][1] = fmaf(qq, d1, D[m][1]);
+                du[0] = fmaf(kk[m], D[m][0], du[0]);
+                du[1] = fmaf(kk[m], D[m][1], du[1]);
+                pdq[m] = p.scale * (fmaf(kk[m], b * rr.x, sp[m][0]) * d0 + fmaf(kk[m], b * rr.y, sp[m][1]) * d1);
+            }
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) {
+                du[0] += __shfl_xor_sync(0xffffffffu, du[0], d);
+                du[1] += __shfl_xor_sync(0xffffffffu, du[1], d);
+            }
+            const float v0 = b * du[0], v1 = b * du[1];
+            float pdb = rg == 0 ? du[0] * rr.x + du[1] * rr.y : 0.f, pdg = 0.f, pdk[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                pdk[m] = D[m][0] * (b * rr.x) + D[m][1] * (b * rr.y) - sp[m][0] * v0 - sp[m][1] * v1;
+                const float e0 = fmaf(-kk[m], v0, D[m][0]), e1 = fmaf(-kk[m], v1, D[m][1]);
+                pdg = fmaf(e0, sp[m][0], fmaf(e1, sp[m][1], pdg));
+                D[m][0] = a * e0;
+                D[m][1] = a * e1;
+            }
+#pragma unroll
+            for (int d = 1; d < 4; d *= 2)
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    pdq[m] += __shfl_xor_sync(0xffffffffu, pdq[m], d);
+                    pdk[m] += __shfl_xor_sync(0xffffffffu, pdk[m], d);
+                }
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                pdb += __shfl_xor_sync(0xffffffffu, pdb, d);
+                pdg += __shfl_xor_sync(0xffffffffu, pdg, d);
+            }
+            float *pp = part + (i * 8 + warp) * kPart;
+            if ((lane & 3) == 0) {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    pp[row + m] = pdq[m];
+                    pp[kN + row + m] = pdk[m];
+                }
+            }
+            if (lane == 0) {
+                pp[2 * kN] = pdb;
+                pp[2 * kN + 1] = pdg;
+            }
+            if (rg == 0) {
+                wr(dv + th * kN + col, v0);
+                wr(dv + th * kN + col + 1, v1);
+            }
+        }
+        __syncthreads();
+        for (int e = tid; e < cnt * kPart; e += kThreads) {
+            const int i = e / kPart, x = e % kPart;
+            float sum = 0.f;
+            for (int w = 0; w < 8; ++w) sum += part[(i * 8 + w) * kPart + x];
+            const int64_t t = t0 + i, th = t * p.H + h;
+            if (x >= 2 * kN) wr((x == 2 * kN ? dbeta : dg) + th, sum);
+            else if (p.dq_h) (x < kN ? p.dq_h : p.dk_h)[th * kN + (x & (kN - 1))] = sum;
+            else wr((x < kN ? dq : dk) + th * kN + (x & (kN - 1)), sum);
+        }
+        __syncthreads();
+    }
+    if (p.ds0) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+            *reinterpret_cast<float2 *>(p.ds0 + base + (row + m) * kN + col) = make_float2(D[m][0], D[m][1]);
+    }
+}
+
+// dq and dk of a key head: the shares of its value heads, added in order.  With offsets, only
+// the tokens some sequence holds (the shares of the others were never written).
+template <typename T>
+__global__ void __launch_bounds__(256)
+delta_sum_heads_kernel(int64_t ntok, int64_t Hk, int64_t H, int64_t nseq, const int32_t *__restrict__ offsets,
+                       const float *__restrict__ dq_h, const float *__restrict__ dk_h, T *__restrict__ dq,
+                       T *__restrict__ dk)
+{
+    const int64_t e = blockIdx.x * 256LL + threadIdx.x;  // token, key head, channel
+    const int64_t t = e / (Hk * kN), hk = e / kN % Hk;
+    if (t >= ntok) return;
+    if (offsets) {  // the last sequence that starts at or before t
+        int64_t lo = 0, hi = nseq;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (offsets[mid] <= t) lo = mid + 1;
+            else hi = mid;
+        }
+        if (lo == 0 || t >= offsets[lo]) return;
+    }
+    const int64_t G = H / Hk;
+    float a = 0.f, b = 0.f;
+    for (int64_t i = 0; i < G; ++i) {
+        const int64_t x = (t * H + hk * G + i) * kN + e % kN;
+        a += dq_h[x];
+        b += dk_h[x];
+    }
+    wr(dq + e, a);
+    wr(dk + e, b);
+}
+
+int64_t checkpoints(const DeltaArgs &a)
+{
+    return a.offsets ? a.T / kSeg + a.nseq : a.B * ((a.T + kSeg - 1) / kSeg + 1);
+}
+
+template <typename T> cudaError_t launch(const DeltaBwdArgs &a, cudaStream_t s)
+{
+    const DeltaArgs &f = a.f;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev]) {  // racing first calls set the same attribute: harmless
+        e = cudaFuncSetAttribute(delta_walks_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    const int64_t ntok = f.B * f.T, nck = checkpoints(f);
+    float *ck = static_cast<float *>(a.workspace);
+    float *share = f.H == f.Hk ? nullptr : ck + nck * f.H * kN * kN;
+    const WalkParams p{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, f.scale, f.s0, a.dsT, a.ds0, ck,
+                       share, share ? share + ntok * f.H * kN : nullptr, nck, f.status};
+    delta_walks_kernel<T><<<static_cast<unsigned>(f.nseq * f.H), kThreads, kSmemBytes, s>>>(
+        p, static_cast<const T *>(f.q), static_cast<const T *>(f.k), static_cast<const T *>(f.v),
+        static_cast<const T *>(f.g), static_cast<const T *>(f.beta), static_cast<const T *>(a.dout),
+        static_cast<T *>(a.dq), static_cast<T *>(a.dk), static_cast<T *>(a.dv), static_cast<T *>(a.dg),
+        static_cast<T *>(a.dbeta));
+    e = cudaGetLastError();
+    if (e == cudaSuccess && share && ntok > 0) {
+        const int64_t blocks = (ntok * f.Hk * kN + 255) / 256;
+        if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        delta_sum_heads_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, s>>>(
+            ntok, f.Hk, f.H, f.nseq, f.offsets, share, share + ntok * f.H * kN, static_cast<T *>(a.dq),
+            static_cast<T *>(a.dk));
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+
+size_t delta_walks_workspace_bytes(const DeltaArgs &a)
+{
+    const int64_t shares = a.H == a.Hk ? 0 : 2 * a.B * a.T * a.H * kN;
+    return static_cast<size_t>(checkpoints(a) * a.H * kN * kN + shares) * sizeof(float);
+}
+
+cudaError_t delta_backward_walks_launch(const DeltaBwdArgs &a, cudaStream_t s)
+{
+    if (a.f.nseq * a.f.H == 0) return cudaSuccess;
+    return a.f.bf16 ? launch<__nv_bfloat16>(a, s) : launch<float>(a, s);
+}
+
+}  // namespace wkv

@@ -323,6 +323,154 @@ int wkv6_noalloc_entry(int64_t B, int64_t T, int64_t H, int64_t N, const void *r
     return RWKV_OK;
 }
 
+// ---- gated delta rule ----------------------------------------------------------------
+
+struct DeltaSizes {
+    int64_t n, nk, nh, ns;  // elements of v (and o), of q (and k), of g (and beta), of the states
+    int64_t nseq, nslots;
+};
+
+// Sizes of a delta-rule call, checked for sign, overflow and what the kernels' grids hold.
+int delta_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t nseq, bool packed, int64_t nslots,
+                bool slots, DeltaSizes *z)
+{
+    if (B < 0 || T < 0 || Hk < 0 || H < 0 || N < 0 || (packed && nseq < 0) || (slots && nslots < 0))
+        return fail(RWKV_ERR_SHAPE, "negative size%s");
+    if (packed && B != 1) return fail(RWKV_ERR_SHAPE, "packed sequences (offsets) need B = 1%s");
+    if (H > 0 && (Hk == 0 || H % Hk != 0)) return fail(RWKV_ERR_SHAPE, "Hk must divide H%s");
+    z->nseq = packed ? nseq : B;
+    z->nslots = slots ? nslots : z->nseq;
+    int64_t BT, x;
+    if (!mul_ok(B, T, &BT) || !mul_ok(BT, Hk, &x) || !mul_ok(x, N, &z->nk) || !mul_ok(BT, H, &z->nh) ||
+        !mul_ok(z->nh, N, &z->n) || !mul_ok(z->nslots, H, &x) || !mul_ok(x, N * N, &z->ns) ||
+        !mul_ok(z->nseq, H, &x))
+        return fail(RWKV_ERR_SHAPE, "size product overflows%s");
+    // blocks are numbered by (sequence, head); token, head and slot indices are 32-bit
+    if (x > 0x7fffffffLL || BT > 0x7fffff00LL || z->nslots > 0x7fffffffLL || z->nseq > 0x7ffffffeLL)
+        return fail(RWKV_ERR_SHAPE, "more than 2^31 (sequence, head) pairs, tokens or slots%s");
+    return RWKV_OK;
+}
+
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+int delta_entry(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const void *q, const void *k, const void *v,
+                const void *g, const void *beta, float scale, int64_t nseq, const int32_t *offsets, int64_t nslots,
+                const int32_t *slots, const float *s0, void *o, float *sT, bool bf16)
+{
+    tl_err[0] = 0;
+    DeltaSizes z;
+    int rc = delta_sizes(B, T, Hk, H, N, nseq, offsets != nullptr, nslots, slots != nullptr, &z);
+    if (rc) return rc;
+    if (z.nseq == 0 || H == 0 || N == 0 || (z.n == 0 && !(sT && z.ns > 0))) return RWKV_OK;
+    if (N != 64) return fail(RWKV_ERR_UNSUPPORTED, "head size N must be 64%s");
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(RWKV_ERR_ARG, "scale must be finite%s");
+    if (z.n > 0 && (!q || !k || !v || !g || !beta || !o))
+        return fail(RWKV_ERR_NULL, "q, k, v, g, beta and o must be non-null%s");
+    const void *ptrs[] = {q, k, v, g, beta, s0, o, sT};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return fail(RWKV_ERR_ALIGN, "tensor pointers must be 16-byte aligned%s");
+    if (!aligned4(offsets) || !aligned4(slots)) return fail(RWKV_ERR_ALIGN, "index arrays must be 4-byte aligned%s");
+    const int64_t esz = bf16 ? 2 : 4;
+    const Span so{o, z.n * esz}, ss0{s0, z.ns * 4}, ssT{sT, z.ns * 4};
+    const Span ins[] = {{q, z.nk * esz}, {k, z.nk * esz}, {v, z.n * esz}, {g, z.nh * esz}, {beta, z.nh * esz},
+                        {offsets, (z.nseq + 1) * 4}, {slots, z.nseq * 4}};
+    for (const Span &x : ins) {
+        if (overlap(so, x)) return fail(RWKV_ERR_ALIAS, "o overlaps an input%s");
+        if (overlap(ssT, x)) return fail(RWKV_ERR_ALIAS, "sT overlaps an input%s");
+    }
+    if (overlap(so, ss0) || overlap(so, ssT)) return fail(RWKV_ERR_ALIAS, "o overlaps a state%s");
+    if (s0 != sT && overlap(ssT, ss0)) return fail(RWKV_ERR_ALIAS, "sT partially overlaps s0%s");
+    int *status = nullptr;
+    rc = status_word(&status);
+    if (rc) return rc;
+    const wkv::DeltaArgs a{B, T, Hk, H, z.nseq, offsets, z.nslots, slots, q, k, v, g, beta, scale, s0, o, sT, bf16, status};
+    const cudaError_t e = wkv::delta_recurrent_launch(a, tl_stream);
+    return e == cudaSuccess ? RWKV_OK : cuda_fail(e, "delta launch");
+}
+
+int delta_bwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t nseq, bool packed, bool bf16,
+                    DeltaSizes *z, size_t *bytes)
+{
+    int rc = delta_sizes(B, T, Hk, H, N, nseq, packed, 0, false, z);
+    if (rc) return rc;
+    int64_t per, all;  // the largest workspace: a 64 x 64 fp32 state every 8 tokens and two fp32 shares
+    if (!mul_ok(T / 8 + z->nseq + 2, H, &per) || !mul_ok(per, B > 0 ? B : 1, &all) || !mul_ok(all, 8192, &all))
+        return fail(RWKV_ERR_SHAPE, "workspace size overflows%s");
+    wkv::DeltaArgs a{};
+    a.B = B, a.T = T, a.Hk = Hk, a.H = H, a.nseq = z->nseq, a.bf16 = bf16;
+    static const int32_t any = 0;
+    a.offsets = packed ? &any : nullptr;  // only its being there counts
+    *bytes = z->nseq > 0 && z->nh > 0 && N == 64 ? wkv::delta_walks_workspace_bytes(a) : 0;
+    return RWKV_OK;
+}
+
+int delta_bwd_entry(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const void *q, const void *k,
+                    const void *v, const void *g, const void *beta, float scale, int64_t nseq, const int32_t *offsets,
+                    const float *s0, const void *dout, const float *dsT, void *dq, void *dk, void *dv, void *dg,
+                    void *dbeta, float *ds0, void *workspace, size_t wbytes, bool bf16)
+{
+    tl_err[0] = 0;
+    DeltaSizes z;
+    size_t need = 0;
+    int rc = delta_bwd_bytes(B, T, Hk, H, N, nseq, offsets != nullptr, bf16, &z, &need);
+    if (rc) return rc;
+    if (z.nseq == 0 || H == 0 || N == 0 || (z.n == 0 && !(ds0 && z.ns > 0))) return RWKV_OK;
+    if (N != 64) return fail(RWKV_ERR_UNSUPPORTED, "head size N must be 64%s");
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(RWKV_ERR_ARG, "scale must be finite%s");
+    if (z.n > 0 && (!q || !k || !v || !g || !beta || !dout))
+        return fail(RWKV_ERR_NULL, "q, k, v, g, beta and dout must be non-null%s");
+    if (z.n > 0 && (!dq || !dk || !dv || !dg || !dbeta))
+        return fail(RWKV_ERR_NULL, "dq, dk, dv, dg and dbeta must be non-null%s");
+    if (need > 0 && !workspace) return fail(RWKV_ERR_NULL, "workspace must be non-null%s");
+    if (wbytes < need) {
+        snprintf(tl_err, sizeof(tl_err), "workspace holds %zu bytes; this call needs %zu", wbytes, need);
+        return RWKV_ERR_ARG;
+    }
+    const void *ptrs[] = {q, k, v, g, beta, s0, dout, dsT, dq, dk, dv, dg, dbeta, ds0, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return fail(RWKV_ERR_ALIGN, "tensor pointers must be 16-byte aligned%s");
+    if (!aligned4(offsets)) return fail(RWKV_ERR_ALIGN, "index arrays must be 4-byte aligned%s");
+    const int64_t e = bf16 ? 2 : 4;
+    const Span ins[] = {{q, z.nk * e}, {k, z.nk * e}, {v, z.n * e}, {g, z.nh * e}, {beta, z.nh * e}, {s0, z.ns * 4},
+                        {dout, z.n * e}, {dsT, z.ns * 4}, {offsets, (z.nseq + 1) * 4}};
+    const Span outs[] = {{dq, z.nk * e}, {dk, z.nk * e}, {dv, z.n * e}, {dg, z.nh * e}, {dbeta, z.nh * e},
+                         {ds0, z.ns * 4}, {workspace, static_cast<int64_t>(need)}};
+    const int n_outs = sizeof(outs) / sizeof(outs[0]);
+    for (int i = 0; i < n_outs; ++i) {
+        for (const Span &x : ins) {
+            // ds0 may be the very same array as dsT (in place); any other overlap is refused
+            if (outs[i].p == ds0 && x.p == dsT && ds0 == dsT) continue;
+            if (overlap(outs[i], x)) return fail(RWKV_ERR_ALIAS, "a gradient or the workspace overlaps an input%s");
+        }
+        for (int c = i + 1; c < n_outs; ++c)
+            if (overlap(outs[i], outs[c])) return fail(RWKV_ERR_ALIAS, "two outputs overlap%s");
+    }
+    int *status = nullptr;
+    rc = status_word(&status);
+    if (rc) return rc;
+    wkv::DeltaBwdArgs a{};
+    a.f = wkv::DeltaArgs{B, T, Hk, H, z.nseq, offsets, z.nseq, nullptr, q, k, v, g, beta, scale, s0, nullptr, nullptr, bf16, status};
+    a.dout = dout, a.dsT = dsT, a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.ds0 = ds0;
+    a.workspace = workspace;
+    const cudaError_t err = wkv::delta_backward_walks_launch(a, tl_stream);
+    return err == cudaSuccess ? RWKV_OK : cuda_fail(err, "delta backward launch");
+}
+
+// ---- state pools ----------------------------------------------------------------------
+
+int pool_sizes(int64_t layers, int64_t nslots, int64_t slot_bytes, const void *pool, int64_t *bytes)
+{
+    int64_t per;
+    if (layers < 0 || nslots < 0 || slot_bytes < 0) return fail(RWKV_ERR_SHAPE, "negative size%s");
+    if (!mul_ok(nslots, slot_bytes, &per) || !mul_ok(layers, per, bytes))
+        return fail(RWKV_ERR_SHAPE, "size product overflows%s");
+    if (nslots > 0x7fffffffLL) return fail(RWKV_ERR_SHAPE, "more than 2^31 slots%s");
+    if (*bytes > 0 && !pool) return fail(RWKV_ERR_NULL, "pool must be non-null%s");
+    if (slot_bytes % 16 != 0 || !aligned16(pool))
+        return fail(RWKV_ERR_ALIGN, "the pool must be 16-byte aligned and slot_bytes a multiple of 16%s");
+    return RWKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -433,6 +581,94 @@ int rwkv_wkv6_backward_omega_bf16(int64_t B, int64_t T, int64_t H, int64_t N, co
 {
     return wkv6_bwd_entry(B, T, H, N, r, k, v, omega, u, s0, dy, dsT, dr, dk, dv, domega, du, ds0, workspace,
                           workspace_bytes, true, true);
+}
+
+int rwkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const float *q, const float *k,
+                       const float *v, const float *g, const float *beta, float scale, int64_t nseq,
+                       const int32_t *offsets, int64_t nslots, const int32_t *slots, const float *s0, float *o,
+                       float *sT)
+{
+    return delta_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, nslots, slots, s0, o, sT, false);
+}
+
+int rwkv_delta_forward_bf16(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const uint16_t *q,
+                            const uint16_t *k, const uint16_t *v, const uint16_t *g, const uint16_t *beta,
+                            float scale, int64_t nseq, const int32_t *offsets, int64_t nslots, const int32_t *slots,
+                            const float *s0, uint16_t *o, float *sT)
+{
+    return delta_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, nslots, slots, s0, o, sT, true);
+}
+
+int rwkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t nseq,
+                                        int packed, int bf16, size_t *bytes)
+{
+    tl_err[0] = 0;
+    if (!bytes) return fail(RWKV_ERR_NULL, "bytes must be non-null%s");
+    DeltaSizes z;
+    return delta_bwd_bytes(B, T, Hk, H, N, nseq, packed != 0, bf16 != 0, &z, bytes);
+}
+
+int rwkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const float *q, const float *k,
+                        const float *v, const float *g, const float *beta, float scale, int64_t nseq,
+                        const int32_t *offsets, const float *s0, const float *dout, const float *dsT, float *dq,
+                        float *dk, float *dv, float *dg, float *dbeta, float *ds0, void *workspace,
+                        size_t workspace_bytes)
+{
+    return delta_bwd_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, s0, dout, dsT, dq, dk, dv, dg,
+                           dbeta, ds0, workspace, workspace_bytes, false);
+}
+
+int rwkv_delta_backward_bf16(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const uint16_t *q,
+                             const uint16_t *k, const uint16_t *v, const uint16_t *g, const uint16_t *beta,
+                             float scale, int64_t nseq, const int32_t *offsets, const float *s0,
+                             const uint16_t *dout, const float *dsT, uint16_t *dq, uint16_t *dk, uint16_t *dv,
+                             uint16_t *dg, uint16_t *dbeta, float *ds0, void *workspace, size_t workspace_bytes)
+{
+    return delta_bwd_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, s0, dout, dsT, dq, dk, dv, dg,
+                           dbeta, ds0, workspace, workspace_bytes, true);
+}
+
+int rwkv_state_copy(int64_t layers, int64_t nslots, int64_t slot_bytes, void *pool, int64_t n, const int32_t *src,
+                    const int32_t *dst)
+{
+    tl_err[0] = 0;
+    int64_t bytes;
+    int rc = pool_sizes(layers, nslots, slot_bytes, pool, &bytes);
+    if (rc) return rc;
+    if (n < 0 || n > wkv::kMaxCopyPairs) return fail(RWKV_ERR_SHAPE, "n must be 0 .. 4096 pairs%s");
+    if (n == 0 || bytes == 0) return RWKV_OK;
+    if (!src || !dst) return fail(RWKV_ERR_NULL, "src and dst must be non-null%s");
+    if (!aligned4(src) || !aligned4(dst)) return fail(RWKV_ERR_ALIGN, "index arrays must be 4-byte aligned%s");
+    if (overlap({pool, bytes}, {src, n * 4}) || overlap({pool, bytes}, {dst, n * 4}))
+        return fail(RWKV_ERR_ALIAS, "the pool overlaps an index array%s");
+    int *status = nullptr;
+    rc = status_word(&status);
+    if (rc) return rc;
+    const cudaError_t e = wkv::state_copy_launch(
+        {layers, nslots, slot_bytes, static_cast<unsigned char *>(pool), n, src, dst, status}, tl_stream);
+    return e == cudaSuccess ? RWKV_OK : cuda_fail(e, "state copy launch");
+}
+
+int rwkv_state_compact(int64_t layers, int64_t nslots, int64_t slot_bytes, void *pool, const uint8_t *live,
+                       int32_t *new_index, int32_t *count)
+{
+    tl_err[0] = 0;
+    int64_t bytes;
+    int rc = pool_sizes(layers, nslots, slot_bytes, pool, &bytes);
+    if (rc) return rc;
+    if (nslots > wkv::kMaxCompactSlots) return fail(RWKV_ERR_SHAPE, "a compacted pool has at most 16384 slots%s");
+    if (!count || (nslots > 0 && (!live || !new_index)))
+        return fail(RWKV_ERR_NULL, "live, new_index and count must be non-null%s");
+    if (!aligned4(new_index) || !aligned4(count)) return fail(RWKV_ERR_ALIGN, "index arrays must be 4-byte aligned%s");
+    const Span sp{pool, bytes}, sl{live, nslots}, sn{new_index, nslots * 4}, sc{count, 4};
+    if (overlap(sp, sl) || overlap(sp, sn) || overlap(sp, sc) || overlap(sl, sn) || overlap(sl, sc) || overlap(sn, sc))
+        return fail(RWKV_ERR_ALIAS, "the pool, live, new_index and count must not overlap%s");
+    int *status = nullptr;
+    rc = status_word(&status);
+    if (rc) return rc;
+    const cudaError_t e = wkv::state_compact_launch(
+        {layers, nslots, slot_bytes, static_cast<unsigned char *>(pool), live, new_index, count, status}, tl_stream);
+    return e == cudaSuccess ? RWKV_OK : cuda_fail(e, "state compact launch");
 }
 
 int rwkv_set_wkv6_algo(int algo)

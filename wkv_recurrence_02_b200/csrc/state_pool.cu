@@ -1,0 +1,298 @@
+// state_pool.cu -- copying, forking, freeing and compacting slots of a pool of states.
+//
+// A pool is [layers, nslots, slot_bytes].  Both kernels work on byte ranges: a task is one range
+// of W bytes of one layer, taken for all the slots of the call together.  What happens to one
+// byte range never depends on another, so a block needs no agreement with other blocks:
+//   copy     every source's range is loaded into shared memory before any destination's is
+//            written, so the call acts as if all sources were read first (swaps, cycles and
+//            shifts included), with no scratch in global memory.  A source named by several
+//            pairs (a fork) is loaded once.  Of several pairs with one destination the last counts.
+//   compact  the j-th live slot moves to slot j.  A destination lies at or before its source,
+//            so a batch of moves, loaded whole before it is stored, never overwrites a source
+//            of a later batch, and the next batch may load while this one is stored.
+//
+// Both are bound by the bytes: data goes global -> shared -> global by bulk copies and never
+// passes through registers.  One warp moves the data (each lane issues the copies of its own
+// pairs) through two stages, so one task loads while the other is stored; blocks stay
+// resident and take tasks in turn.
+#include "tc_common.cuh"
+
+#include <algorithm>
+
+namespace wkv {
+namespace {
+using namespace tc;
+
+constexpr int kThreads = 256;
+constexpr uint32_t kWaitLimit = 100000;
+constexpr int kCopySmem = 224 * 1024;      // the copy kernel's block owns an SM
+constexpr int kZeroBytes = 8 * 1024;       // zeros for freed slots, and the largest copy range
+constexpr int kCompactStage = 32 * 1024;   // two stages, three blocks per SM
+
+struct CopyParams {
+    StateCopyArgs a;
+    int64_t range;          // bytes of one task's range (a multiple of 16)
+    int64_t per_layer;      // ranges per layer
+    int stage;              // bytes of one of the two stages
+};
+
+// Shared memory: the two stages, zeros, then per pair its source and destination, the pair that
+// loads its source (itself, an earlier one, -1: zeros, -2: the pair does nothing) and, for a
+// loading pair, its place in the stage.
+__global__ void __launch_bounds__(kThreads)
+state_copy_kernel(const CopyParams p)
+{
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+    unsigned char *zeros = sm + 2 * p.stage;
+    __shared__ uint64_t bars[2];
+    __shared__ int nload;
+    const int n = static_cast<int>(p.a.n), tid = threadIdx.x;
+    int *src = reinterpret_cast<int *>(zeros + kZeroBytes), *dst = src + n, *from = dst + n, *pos = from + n;
+    const int nslots = static_cast<int>(p.a.nslots);
+
+    for (int i = tid; i < n; i += kThreads) {
+        int s = p.a.src[i], d = p.a.dst[i];
+        if (s >= nslots || d >= nslots) {  // outside the pool: the pair is left out
+            record_status(p.a.status, kStatusArg);
+            d = -1;
+        }
+        src[i] = s < 0 ? -1 : s;
+        dst[i] = d < 0 ? -1 : d;
+    }
+    for (int i = tid; i < kZeroBytes / 16; i += kThreads) reinterpret_cast<uint4 *>(zeros)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) {
+        nload = 0;
+        bar_init(smem_u32(&bars[0]), 1);
+        bar_init(smem_u32(&bars[1]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    // a pair whose destination a later pair names again does nothing, nor does one that names
+    // its own slot; a pair's source is loaded by the first pair that still has it
+    for (int i = tid; i < n; i += kThreads) {
+        const int d = dst[i];
+        int dead = d < 0 || d == src[i];
+        for (int j = i + 1; j < n && !dead; ++j) dead = dst[j] == d;
+        from[i] = dead ? -2 : -1;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+        const int s = src[i];
+        if (from[i] == -2 || s < 0) continue;
+        int j = 0;
+        while (j < i && !(src[j] == s && from[j] != -2)) ++j;
+        from[i] = j;  // never -2 or -1, so a concurrent reader's test above is unchanged
+    }
+    __syncthreads();
+    fence_async_smem();  // the zeros are read by bulk stores
+    // stage positions in pair order: position of pair i's own load = loading pairs before it
+    if (tid < 32) {
+        int count = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + tid;
+            const bool loads = i < n && from[i] == i;
+            const unsigned m = __ballot_sync(0xffffffffu, loads);
+            if (loads) pos[i] = count + __popc(m & ((1u << tid) - 1));
+            count += __popc(m);
+        }
+        if (tid == 0) nload = count;
+    }
+    __syncthreads();
+    if (tid >= 32) return;
+    const int lane = tid;
+    const int64_t tasks = p.a.layers * p.per_layer;
+    const int64_t layer_bytes = p.a.nslots * p.a.slot_bytes;
+    const int64_t pool_bytes = p.a.layers * layer_bytes;
+    auto load = [&](int64_t task, int st) {
+        const int64_t layer = task / p.per_layer, off = task % p.per_layer * p.range;
+        const uint32_t w = static_cast<uint32_t>(min(p.range, p.a.slot_bytes - off));
+        const uint32_t bar = smem_u32(&bars[st]);
+        if (lane == 0) bar_expect_tx(bar, w * nload);
+        __syncwarp();
+        for (int i = lane; i < n; i += 32)
+            if (from[i] == i) {
+                const int64_t at = layer * layer_bytes + src[i] * p.a.slot_bytes + off;
+                if (in_bounds(p.a.status, at, w, pool_bytes) &&
+                    in_bounds(p.a.status, pos[i] * p.range, w, p.stage))
+                    bulk_load(smem_u32(sm + st * p.stage + pos[i] * p.range), p.a.pool + at, w, bar);
+            }
+    };
+    int64_t it = 0;
+    bool ok = true;
+    if (blockIdx.x < tasks) load(blockIdx.x, 0);
+    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x, ++it) {
+        const int st = static_cast<int>(it & 1);
+        if (task + gridDim.x < tasks) {
+            bulk_wait_read<0>();  // this lane's stores of the task before have read the other stage
+            __syncwarp();
+            load(task + gridDim.x, st ^ 1);
+        }
+        ok = bar_wait(smem_u32(&bars[st]), static_cast<uint32_t>((it >> 1) & 1), kWaitLimit);
+        if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) record_status(p.a.status, kStatusTimeout);
+            bar_wait(smem_u32(&bars[st ^ 1]), static_cast<uint32_t>(((it + 1) >> 1) & 1), kWaitLimit);  // the copies in flight
+            break;
+        }
+        const int64_t layer = task / p.per_layer, off = task % p.per_layer * p.range;
+        const uint32_t w = static_cast<uint32_t>(min(p.range, p.a.slot_bytes - off));
+        for (int i = lane; i < n; i += 32) {
+            const int f = from[i];
+            if (f == -2) continue;
+            const int64_t at = layer * layer_bytes + dst[i] * p.a.slot_bytes + off;
+            if (in_bounds(p.a.status, at, w, pool_bytes))
+                bulk_store(p.a.pool + at, smem_u32(f < 0 ? zeros : sm + st * p.stage + pos[f] * p.range), w);
+        }
+        bulk_commit();
+    }
+    bulk_wait_all();
+}
+
+struct CompactParams {
+    StateCompactArgs a;
+    int64_t range, per_layer;
+    int batch;              // moves per stage
+};
+
+__global__ void __launch_bounds__(kThreads)
+state_compact_kernel(const CompactParams p)
+{
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+    uint16_t *list = reinterpret_cast<uint16_t *>(sm + 2 * kCompactStage);  // live slots in order
+    __shared__ uint64_t bars[2];
+    __shared__ int warp_sum[kThreads / 32], s_first;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nslots = static_cast<int>(p.a.nslots);
+    if (tid == 0) {
+        s_first = nslots;
+        bar_init(smem_u32(&bars[0]), 1);
+        bar_init(smem_u32(&bars[1]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    int count = 0;
+    for (int i0 = 0; i0 < nslots; i0 += kThreads) {  // places of the live slots, 256 at a time
+        const int i = i0 + tid;
+        const bool live = i < nslots && p.a.live[i] != 0;
+        const unsigned m = __ballot_sync(0xffffffffu, live);
+        if (lane == 0) warp_sum[warp] = __popc(m);
+        __syncthreads();
+        int at = count + __popc(m & ((1u << lane) - 1));
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) at += warp_sum[w];
+            count += warp_sum[w];
+        }
+        if (live) {
+            list[at] = static_cast<uint16_t>(i);
+            if (at != i) atomicMin(&s_first, at);
+        }
+        if (blockIdx.x == 0 && i < nslots) p.a.new_index[i] = live ? at : -1;
+        __syncthreads();
+    }
+    if (blockIdx.x == 0 && tid == 0) *p.a.count = count;
+    if (warp != 0) return;
+    const int first = s_first;  // moves are live places first .. count - 1
+    if (first >= count) return;
+    const int nb = (count - first + p.batch - 1) / p.batch;  // batches per range
+    const int64_t tasks = p.a.layers * p.per_layer;
+    const int64_t mine = tasks > blockIdx.x ? (tasks - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    const int64_t total = mine * nb;
+    const int64_t layer_bytes = p.a.nslots * p.a.slot_bytes, pool_bytes = p.a.layers * layer_bytes;
+    auto where = [&](int64_t it, int64_t *base, uint32_t *w, int *m0, int *m1) {
+        const int64_t task = blockIdx.x + it / nb * gridDim.x;
+        const int64_t off = task % p.per_layer * p.range;
+        *base = task / p.per_layer * layer_bytes + off;
+        *w = static_cast<uint32_t>(min(p.range, p.a.slot_bytes - off));
+        *m0 = first + static_cast<int>(it % nb) * p.batch;
+        *m1 = min(*m0 + p.batch, count);
+    };
+    auto load = [&](int64_t it) {
+        int64_t base;
+        uint32_t w;
+        int m0, m1;
+        where(it, &base, &w, &m0, &m1);
+        const int st = static_cast<int>(it & 1);
+        const uint32_t bar = smem_u32(&bars[st]);
+        if (lane == 0) bar_expect_tx(bar, w * (m1 - m0));
+        __syncwarp();
+        for (int m = m0 + lane; m < m1; m += 32) {
+            const int64_t at = base + list[m] * p.a.slot_bytes;
+            if (in_bounds(p.a.status, at, w, pool_bytes) && in_bounds(p.a.status, (m - m0) * p.range, w, kCompactStage))
+                bulk_load(smem_u32(sm + st * kCompactStage + (m - m0) * p.range), p.a.pool + at, w, bar);
+        }
+    };
+    if (total > 0) load(0);
+    for (int64_t it = 0; it < total; ++it) {
+        const int st = static_cast<int>(it & 1);
+        if (it + 1 < total) {
+            bulk_wait_read<0>();  // the other stage's stores have read it
+            __syncwarp();
+            load(it + 1);
+        }
+        const bool ok = bar_wait(smem_u32(&bars[st]), static_cast<uint32_t>((it >> 1) & 1), kWaitLimit);
+        if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) record_status(p.a.status, kStatusTimeout);
+            bar_wait(smem_u32(&bars[st ^ 1]), static_cast<uint32_t>(((it + 1) >> 1) & 1), kWaitLimit);  // the copies in flight
+            break;
+        }
+        int64_t base;
+        uint32_t w;
+        int m0, m1;
+        where(it, &base, &w, &m0, &m1);
+        for (int m = m0 + lane; m < m1; m += 32) {
+            const int64_t at = base + m * p.a.slot_bytes;
+            if (in_bounds(p.a.status, at, w, pool_bytes))
+                bulk_store(p.a.pool + at, smem_u32(sm + st * kCompactStage + (m - m0) * p.range), w);
+        }
+        bulk_commit();
+    }
+    bulk_wait_all();
+}
+
+int64_t sms()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 148;
+    return n;
+}
+
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// Largest range of at most `most` bytes (a multiple of 16) that still gives every one of
+// `blocks` blocks a task, but no less than 512 bytes (shorter bulk copies waste their issue).
+int64_t pick_range(int64_t layers, int64_t slot_bytes, int64_t most, int64_t blocks)
+{
+    const int64_t share = round16((layers * slot_bytes + blocks - 1) / blocks);
+    return std::max<int64_t>(16, std::min(most, std::max<int64_t>(share, 512)) / 16 * 16);
+}
+
+}  // namespace
+
+cudaError_t state_copy_launch(const StateCopyArgs &a, cudaStream_t s)
+{
+    const int64_t stage = (kCopySmem - 128 - kZeroBytes - 16 * a.n) / 2 / 128 * 128;
+    const int64_t most = std::min<int64_t>(kZeroBytes, stage / a.n / 16 * 16);
+    const int64_t range = pick_range(a.layers, a.slot_bytes, most, sms());
+    const int64_t per_layer = (a.slot_bytes + range - 1) / range;
+    const cudaError_t e = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopySmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(std::min(a.layers * per_layer, sms()));
+    state_copy_kernel<<<grid, kThreads, kCopySmem, s>>>(CopyParams{a, range, per_layer, static_cast<int>(stage)});
+    return cudaGetLastError();
+}
+
+cudaError_t state_compact_launch(const StateCompactArgs &a, cudaStream_t s)
+{
+    const int64_t blocks = 3 * sms();
+    const int64_t range = pick_range(a.layers, a.slot_bytes, 4096, blocks);
+    const int64_t per_layer = (a.slot_bytes + range - 1) / range;
+    const int smem = 2 * kCompactStage + static_cast<int>(a.nslots) * 2 + 128;
+    const cudaError_t e = cudaFuncSetAttribute(state_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               2 * kCompactStage + static_cast<int>(kMaxCompactSlots) * 2 + 128);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(std::min(std::max<int64_t>(a.layers * per_layer, 1), blocks));
+    state_compact_kernel<<<grid, kThreads, smem, s>>>(CompactParams{a, range, per_layer, static_cast<int>(kCompactStage / range)});
+    return cudaGetLastError();
+}
+
+}  // namespace wkv

@@ -12,6 +12,7 @@ namespace wkv {
 
 // Status codes written by kernels into the device status word (same values as rwkv_status).
 constexpr int kStatusTimeout = -6;
+constexpr int kStatusArg = -8;
 constexpr int kStatusBounds = -9;
 
 // Record the first device-side error; later errors keep the first one.
@@ -161,5 +162,84 @@ cudaError_t wkv6_chunked_launch_noalloc(const Wkv6Args &a, int segments, size_t 
 // Test hook: when nonzero, chunked launches first wait on a barrier that is never
 // signalled (short bound) so the timeout path runs; set via rwkv_debug_inject_timeout.
 extern int g_chunked_inject_timeout;
+
+// Gated delta rule forward.  Sequences are the B batch rows, or (offsets non-null, B = 1) the
+// nseq runs of tokens offsets[i] .. offsets[i + 1] - 1.
+struct DeltaArgs {
+    int64_t B, T, Hk, H;
+    int64_t nseq;               // sequences (B when offsets is null)
+    const int32_t *offsets;     // [nseq + 1] device, or null
+    int64_t nslots;             // states behind s0 / sT (nseq when slots is null)
+    const int32_t *slots;       // [nseq] device: state of each sequence, or null
+    const void *q, *k;          // [B,T,Hk,64] fp32 or bf16
+    const void *v;              // [B,T,H,64]
+    const void *g, *beta;       // [B,T,H]
+    float scale;
+    const float *s0;            // [nslots,H,64,64] or null
+    void *o;                    // [B,T,H,64]
+    float *sT;                  // [nslots,H,64,64] or null
+    bool bf16;
+    int *status;
+};
+cudaError_t delta_recurrent_launch(const DeltaArgs &a, cudaStream_t s);
+
+// Gated delta rule backward; gradients in the type of the inputs, state gradients fp32.
+struct DeltaBwdArgs {
+    DeltaArgs f;                // o, sT and slots unused
+    const void *dout;           // [B,T,H,64]
+    const float *dsT;           // [nseq,H,64,64] or null
+    void *dq, *dk;              // [B,T,Hk,64]
+    void *dv;                   // [B,T,H,64]
+    void *dg, *dbeta;           // [B,T,H]
+    float *ds0;                 // [nseq,H,64,64] or null
+    void *workspace;
+};
+size_t delta_walks_workspace_bytes(const DeltaArgs &a);
+cudaError_t delta_backward_walks_launch(const DeltaBwdArgs &a, cudaStream_t s);
+
+// First token and length of sequence i, clamped to the tokens there are, whatever the offsets say.
+__device__ __forceinline__ void sequence_span(const int32_t *offsets, int64_t i, int64_t T, int64_t *first, int64_t *len)
+{
+    if (!offsets) {
+        *first = i * T;
+        *len = T;
+        return;
+    }
+    const int64_t a = min(max(static_cast<int64_t>(offsets[i]), static_cast<int64_t>(0)), T);
+    const int64_t b = min(max(static_cast<int64_t>(offsets[i + 1]), a), T);
+    *first = a;
+    *len = b - a;
+}
+
+// State slot of sequence i, or -1 where it has none (a negative slot; one past the pool is
+// recorded as RWKV_ERR_ARG).
+__device__ __forceinline__ int64_t sequence_slot(const int32_t *slots, int64_t i, int64_t nslots, int *status)
+{
+    if (!slots) return i;
+    const int64_t s = slots[i];
+    if (s >= nslots) record_status(status, kStatusArg);
+    return s >= 0 && s < nslots ? s : -1;
+}
+
+// State pools: [layers, nslots, slot_bytes].
+struct StateCopyArgs {
+    int64_t layers, nslots, slot_bytes;
+    unsigned char *pool;
+    int64_t n;
+    const int32_t *src, *dst;   // [n] device
+    int *status;
+};
+cudaError_t state_copy_launch(const StateCopyArgs &a, cudaStream_t s);
+struct StateCompactArgs {
+    int64_t layers, nslots, slot_bytes;
+    unsigned char *pool;
+    const uint8_t *live;        // [nslots] device
+    int32_t *new_index;         // [nslots] device
+    int32_t *count;             // [1] device
+    int *status;
+};
+cudaError_t state_compact_launch(const StateCompactArgs &a, cudaStream_t s);
+constexpr int64_t kMaxCopyPairs = 4096;      // pairs of one copy: their indices sit in shared memory
+constexpr int64_t kMaxCompactSlots = 16384;  // slots of a compacted pool: as above
 
 }  // namespace wkv

@@ -7,6 +7,9 @@ not on a CUDA device, the call raises.
 Functions mirror the C entry points:
   wkv4_forward(w, u, k, v, s0=None, want_state=False)   -> y            | (y, sT)
   wkv6_forward(r, k, v, w, u, s0=None, want_state=True) -> (y, sT)      | y
+  delta_forward(q, k, v, g, beta, s0=None, ...)         -> (o, sT)      | o
+  delta_backward(q, k, v, g, beta, do, ...)             -> dict of gradients
+  state_copy(pool, src, dst), state_compact(pool, live) -> None, (new_index, count)
 The calls are asynchronous on torch's current CUDA stream.
 """
 import contextlib
@@ -82,6 +85,22 @@ def load(path: str = LIB_PATH):
     lib.rwkv_wkv6_backward_workspace_bytes.argtypes = [_i64] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.rwkv_wkv6_backward_workspace_bytes.restype = ctypes.c_int
     lib.rwkv_wkv6_forward_bf16_noalloc.restype = ctypes.c_int
+    delta = [_i64] * 5 + [_vp] * 5 + [ctypes.c_float, _i64, _vp]
+    for name in ("rwkv_delta_forward", "rwkv_delta_forward_bf16"):
+        fn = getattr(lib, name)
+        fn.argtypes = delta + [_i64, _vp, _vp, _vp, _vp]
+        fn.restype = ctypes.c_int
+    for name in ("rwkv_delta_backward", "rwkv_delta_backward_bf16"):
+        fn = getattr(lib, name)
+        fn.argtypes = delta + [_vp] * 10 + [ctypes.c_size_t]
+        fn.restype = ctypes.c_int
+    lib.rwkv_delta_backward_workspace_bytes.argtypes = [_i64] * 6 + [ctypes.c_int, ctypes.c_int,
+                                                                     ctypes.POINTER(ctypes.c_size_t)]
+    lib.rwkv_delta_backward_workspace_bytes.restype = ctypes.c_int
+    lib.rwkv_state_copy.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp]
+    lib.rwkv_state_copy.restype = ctypes.c_int
+    lib.rwkv_state_compact.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp]
+    lib.rwkv_state_compact.restype = ctypes.c_int
     lib.rwkv_set_wkv6_segments.argtypes = [ctypes.c_int]
     lib.rwkv_set_wkv6_segments.restype = ctypes.c_int
     lib.rwkv_get_wkv6_segments.argtypes = []
@@ -340,6 +359,171 @@ def wkv6_backward(r, k, v, w, u, dy, s0=None, dsT=None, omega=False, want_ds0=Tr
     if not want_ds0:
         del out["ds0"]
     return out
+
+
+@contextlib.contextmanager
+def _on_device_of(lib, t):
+    """The tensor's device made current, its current torch stream the library's."""
+    with torch.cuda.device(t.device):
+        _use_current_stream(lib, t.device)
+        yield
+
+
+def _same_device(t, **others):
+    for name, x in others.items():
+        if x is not None and x.device != t.device:
+            raise ValueError(f"{name} is on {x.device}, not on {t.device}")
+
+
+def _delta_shapes(q, k, v, g, beta, offsets):
+    """(B, T, Hk, H, N, sequences, dtype) of a delta-rule call, its inputs checked."""
+    _cuda(q, "q")
+    _cuda(v, "v")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must have shape [B, T, heads, N]")
+    B, T, Hk, N = q.shape
+    H, dt = v.shape[2], q.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError("q must be float32 or bfloat16")
+    _cuda(k, "k", dt, (B, T, Hk, N))
+    _cuda(v, "v", dt, (B, T, H, N))
+    _cuda(g, "g", dt, (B, T, H))
+    _cuda(beta, "beta", dt, (B, T, H))
+    nseq = B
+    if offsets is not None:
+        _cuda(offsets, "offsets", torch.int32)
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError("offsets must have shape [sequences + 1]")
+        nseq = offsets.numel() - 1
+    _same_device(q, k=k, v=v, g=g, beta=beta, offsets=offsets)
+    return B, T, Hk, H, N, nseq, dt
+
+
+def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=None, want_state=True, o=None, sT=None):
+    """Gated delta rule: S' = exp(g) S, u = beta (v - k S'), S = S' + k^T u, o = scale q S.
+
+    q, k: [B,T,Hk,N] fp32|bf16; v: [B,T,H,N]; g, beta: [B,T,H] (Hk divides H).  scale: default
+    1/sqrt(N).  offsets: int32 [sequences+1], the runs of tokens of a packed call (B = 1).
+    s0: [sequences,H,N,N] fp32 or None (zero); with slots (int32 [sequences]), a pool
+    [P,H,N,N] whose slot slots[i] is sequence i's state, updated in place unless another pool
+    is given as sT; a negative slot is a sequence without a state.  Returns (o, sT), or o.
+    """
+    lib = load()
+    B, T, Hk, H, N, nseq, dt = _delta_shapes(q, k, v, g, beta, offsets)
+    if slots is not None:
+        _cuda(slots, "slots", torch.int32, (nseq,))
+        if sT is None and want_state:
+            if s0 is None:
+                raise ValueError("slots need a pool: s0, sT or both")
+            sT = s0
+    pool = s0 if s0 is not None else sT
+    nslots = nseq if slots is None or pool is None else pool.shape[0]
+    _cuda(s0, "s0", torch.float32, (nslots, H, N, N))
+    if o is None:
+        o = torch.empty_like(v)
+    _cuda(o, "o", dt, (B, T, H, N))
+    if sT is None and want_state:
+        sT = torch.empty(nseq, H, N, N, device=q.device, dtype=torch.float32)
+    _cuda(sT, "sT", torch.float32, (nslots, H, N, N))
+    _same_device(q, s0=s0, slots=slots, o=o, sT=sT)
+    fn = lib.rwkv_delta_forward_bf16 if dt == torch.bfloat16 else lib.rwkv_delta_forward
+    with _on_device_of(lib, q):
+        _check(fn(B, T, Hk, H, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                  N ** -0.5 if scale is None else float(scale), nseq, _ptr(offsets), nslots, _ptr(slots), _ptr(s0),
+                  _ptr(o), _ptr(sT)))
+    return (o, sT) if want_state else o
+
+
+def delta_backward_workspace_bytes(B, T, Hk, H, N=64, nseq=None, packed=False, bf16=True) -> int:
+    """Device scratch (bytes) that a delta-rule backward call of this shape needs."""
+    lib = load()
+    out = ctypes.c_size_t(0)
+    _check(lib.rwkv_delta_backward_workspace_bytes(int(B), int(T), int(Hk), int(H), int(N),
+                                                   int(B if nseq is None else nseq), int(packed), int(bf16),
+                                                   ctypes.byref(out)))
+    return int(out.value)
+
+
+def delta_backward(q, k, v, g, beta, do, scale=None, s0=None, dsT=None, offsets=None, want_ds0=True, workspace=None):
+    """Gradients of delta_forward for a loss with dL/do = do and dL/dsT = dsT (None = 0).
+
+    Inputs as in delta_forward (no slots); do: [B,T,H,N]; dsT: [sequences,H,N,N] fp32.  Returns
+    a dict of dq, dk, dv, dg, dbeta (type of the inputs) and ds0 (fp32, when want_ds0).
+    Gradients of tokens outside every sequence are zero.  workspace: optional uint8 CUDA tensor
+    of at least delta_backward_workspace_bytes bytes; allocated here when not given.
+    """
+    lib = load()
+    B, T, Hk, H, N, nseq, dt = _delta_shapes(q, k, v, g, beta, offsets)
+    _cuda(do, "do", dt, (B, T, H, N))
+    _cuda(s0, "s0", torch.float32, (nseq, H, N, N))
+    _cuda(dsT, "dsT", torch.float32, (nseq, H, N, N))
+    make = torch.empty_like if offsets is None else torch.zeros_like
+    out = {"dq": make(q), "dk": make(k), "dv": make(v), "dg": make(g), "dbeta": make(beta)}
+    out["ds0"] = torch.empty(nseq, H, N, N, device=q.device, dtype=torch.float32) if want_ds0 else None
+    if workspace is None:
+        need = delta_backward_workspace_bytes(B, T, Hk, H, N, nseq, offsets is not None, dt == torch.bfloat16)
+        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+    _cuda(workspace, "workspace", torch.uint8)
+    _same_device(q, do=do, s0=s0, dsT=dsT, workspace=workspace)
+    fn = lib.rwkv_delta_backward_bf16 if dt == torch.bfloat16 else lib.rwkv_delta_backward
+    with _on_device_of(lib, q):
+        _check(fn(B, T, Hk, H, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                  N ** -0.5 if scale is None else float(scale), nseq, _ptr(offsets), _ptr(s0), _ptr(do), _ptr(dsT),
+                  _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
+                  _ptr(out["ds0"]), _ptr(workspace), ctypes.c_size_t(workspace.numel())))
+    if not want_ds0:
+        del out["ds0"]
+    return out
+
+
+def _pool_shape(pool, slot_dim):
+    """(layers, slots, bytes of a slot) of a pool whose dimension slot_dim counts the slots."""
+    _cuda(pool, "pool")
+    if not 0 <= slot_dim < pool.dim():
+        raise ValueError("slot_dim must be a dimension of the pool")
+    layers = slot = 1
+    for n in pool.shape[:slot_dim]:
+        layers *= n
+    for n in pool.shape[slot_dim + 1:]:
+        slot *= n
+    return layers, pool.shape[slot_dim], slot * pool.element_size()
+
+
+def state_copy(pool, src, dst, slot_dim=0):
+    """Copy, fork and free slots of a pool of states, in place: for every pair, slot dst[i] <-
+    slot src[i] as it was before the call (src[i] < 0: zeros; dst[i] < 0: the pair is left out;
+    of several pairs with one dst the last counts).
+
+    pool: any CUDA tensor whose dimension slot_dim counts the slots and whose earlier ones count
+    layers, e.g. [P,H,N,N], or [L,P,H,N,N] with slot_dim=1.  src, dst: int32 [n], n <= 4096.
+    """
+    lib = load()
+    layers, nslots, slot_bytes = _pool_shape(pool, slot_dim)
+    _cuda(src, "src", torch.int32)
+    _cuda(dst, "dst", torch.int32, src.shape)
+    _same_device(pool, src=src, dst=dst)
+    with _on_device_of(lib, pool):
+        _check(lib.rwkv_state_copy(layers, nslots, slot_bytes, _ptr(pool), src.numel(), _ptr(src), _ptr(dst)))
+
+
+def state_compact(pool, live, slot_dim=0):
+    """Move the live slots of a pool of states to its front, in order and in place.
+
+    pool, slot_dim: as in state_copy, at most 16384 slots; live: bool or uint8 [P].  Returns
+    (new_index, count): int32 [P], the place each slot went to (-1 if it is not live), and
+    int32 [1], both on the device.  Slots from count on keep what they hold.
+    """
+    lib = load()
+    layers, nslots, slot_bytes = _pool_shape(pool, slot_dim)
+    _cuda(live, "live", None, (nslots,))
+    if live.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("live must be bool or uint8")
+    _same_device(pool, live=live)
+    new_index = torch.empty(nslots, device=pool.device, dtype=torch.int32)
+    count = torch.empty(1, device=pool.device, dtype=torch.int32)
+    with _on_device_of(lib, pool):
+        _check(lib.rwkv_state_compact(layers, nslots, slot_bytes, _ptr(pool), _ptr(live), _ptr(new_index), _ptr(count)))
+    return new_index, count
 
 
 def device_status() -> int:
