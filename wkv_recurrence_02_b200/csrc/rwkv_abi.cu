@@ -351,6 +351,9 @@ int delta_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t 
     return RWKV_OK;
 }
 
+// Shortest mean sequence that takes the chunked kernel.
+constexpr int64_t kDeltaChunkedTokens = 16;
+
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
 int delta_entry(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const void *q, const void *k, const void *v,
@@ -384,7 +387,8 @@ int delta_entry(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const vo
     rc = status_word(&status);
     if (rc) return rc;
     const wkv::DeltaArgs a{B, T, Hk, H, z.nseq, offsets, z.nslots, slots, q, k, v, g, beta, scale, s0, o, sT, bf16, status};
-    const cudaError_t e = wkv::delta_recurrent_launch(a, tl_stream);
+    const bool chunked = bf16 && z.n > 0 && (offsets ? T / z.nseq : T) >= kDeltaChunkedTokens;
+    const cudaError_t e = chunked ? wkv::delta_chunked_launch(a, tl_stream) : wkv::delta_recurrent_launch(a, tl_stream);
     return e == cudaSuccess ? RWKV_OK : cuda_fail(e, "delta launch");
 }
 

@@ -182,6 +182,7 @@ struct DeltaArgs {
     int *status;
 };
 cudaError_t delta_recurrent_launch(const DeltaArgs &a, cudaStream_t s);
+cudaError_t delta_chunked_launch(const DeltaArgs &a, cudaStream_t s);  // bf16, B * T > 0
 
 // Gated delta rule backward; gradients in the type of the inputs, state gradients fp32.
 struct DeltaBwdArgs {
