@@ -256,19 +256,31 @@ int rwkv_wkv6_backward_omega_bf16(int64_t B, int64_t T, int64_t H, int64_t N,
  *             word.  A slot named by two sequences of one call ends with the state of one
  *             of them, or, in place, of either started from any mix of the two: name each
  *             slot once (rwkv_state_copy forks states).  nslots is ignored without slots.
+ *   workspace : device scratch owned by the caller, 16-byte aligned, of at least the bytes
+ *             that rwkv_delta_forward_workspace_bytes reports for the same sizes (packed:
+ *             offsets given; bf16: the entry point's type); fewer are refused with
+ *             RWKV_ERR_ARG.  Zero bytes (workspace may be NULL) for fp32 and for short
+ *             sequences.  No initialisation needed, undefined afterwards; calls whose work
+ *             overlaps need a workspace each.
  *   N must be 64.  Index arrays are 4-byte aligned; other rules and errors as above.
- * Accumulation is fp32 and the state is held in fp32 throughout.
+ * Accumulation is fp32 and the state is held in fp32 throughout.  bf16 sequences of 16 tokens
+ * or more (packed: on average) run in 64-token chunks on the tensor cores: there the output
+ * is formed from bf16 operands, and every operand of the state from two bf16 terms (2^-16 of
+ * its value).  Others run token by token in fp32.
  */
+int rwkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
+                                       int64_t nseq, int packed, int bf16, size_t *bytes);
 int rwkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
                        const float *q, const float *k, const float *v, const float *g,
                        const float *beta, float scale, int64_t nseq, const int32_t *offsets,
                        int64_t nslots, const int32_t *slots, const float *s0, float *o,
-                       float *sT);
+                       float *sT, void *workspace, size_t workspace_bytes);
 int rwkv_delta_forward_bf16(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N,
                             const uint16_t *q, const uint16_t *k, const uint16_t *v,
                             const uint16_t *g, const uint16_t *beta, float scale, int64_t nseq,
                             const int32_t *offsets, int64_t nslots, const int32_t *slots,
-                            const float *s0, uint16_t *o, float *sT);
+                            const float *s0, uint16_t *o, float *sT, void *workspace,
+                            size_t workspace_bytes);
 
 /* Backward pass of the gated delta rule.  Given dout = dL/do ([B, T, H, N], type of q) and
  * dsT = dL/dsT ([nseq, H, N, N] fp32, NULL = 0) it writes, with D the gradient of the state

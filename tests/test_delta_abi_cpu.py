@@ -21,16 +21,16 @@ def _p(i, off=0):
     return ctypes.c_void_p(FAKE + i * STEP + off)
 
 
-FWD = ["q", "k", "v", "g", "beta", "offsets", "slots", "s0", "o", "sT"]
+FWD = ["q", "k", "v", "g", "beta", "offsets", "slots", "s0", "o", "sT", "ws"]
 
 
-def _forward(lib, bf16=True, B=1, T=8, Hk=2, H=4, N=64, scale=0.125, nseq=2, nslots=4, **kw):
+def _forward(lib, bf16=True, B=1, T=8, Hk=2, H=4, N=64, scale=0.125, nseq=2, nslots=4, wbytes=STEP, **kw):
     a = {n: _p(i) for i, n in enumerate(FWD)}
     a["offsets"] = a["slots"] = None
     a.update(kw)
     fn = lib.rwkv_delta_forward_bf16 if bf16 else lib.rwkv_delta_forward
     return fn(B, T, Hk, H, N, a["q"], a["k"], a["v"], a["g"], a["beta"], scale, nseq, a["offsets"], nslots,
-              a["slots"], a["s0"], a["o"], a["sT"])
+              a["slots"], a["s0"], a["o"], a["sT"], a["ws"], ctypes.c_size_t(wbytes))
 
 
 @pytest.mark.parametrize("bf16", [True, False])
@@ -56,6 +56,22 @@ def test_forward_refusals(lib, bf16):
     assert f(offsets=_p(5), o=_p(5)) == -4 and f(slots=_p(6), sT=_p(6)) == -4
     assert f(o=_p(7)) == -4 and f(o=_p(9)) == -4                # o over a state
     assert f(sT=_p(7, 64)) == -4                                # sT partly over s0
+    assert f(ws=_p(10, 8)) == -7
+
+
+def test_forward_workspace(lib):
+    need = ctypes.c_size_t(7)
+    size = lambda T, bf16, packed=0, nseq=1, B=1: (lib.rwkv_delta_forward_workspace_bytes(  # noqa: E731
+        B, T, 2, 4, 64, nseq, packed, bf16, ctypes.byref(need)), need.value)
+    assert size(1, 1) == (0, 0) and size(15, 1) == (0, 0) and size(4096, 0) == (0, 0) and size(0, 1) == (0, 0)
+    rc, n = size(200, 1)
+    assert rc == 0 and n > 0
+    assert size(200, 1, 1, 200)[1] == 0                         # packed: one token each on average
+    assert size(8, 1, B=-1)[0] == -2
+    f = lambda **kw: _forward(lib, True, T=200, **kw)  # noqa: E731
+    assert f(wbytes=n - 1) == -8 and f(ws=None) == -1
+    for i in FWD[:5] + ["s0", "o", "sT"]:
+        assert f(ws=_p(FWD.index(i))) == -4, i
 
 
 def test_forward_nothing_to_do(lib):

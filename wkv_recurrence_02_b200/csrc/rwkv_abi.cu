@@ -356,39 +356,78 @@ constexpr int64_t kDeltaChunkedTokens = 16;
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
+// A DeltaArgs with the sizes alone, for the workspace of a call.
+wkv::DeltaArgs delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t H, const DeltaSizes &z, bool packed, bool bf16)
+{
+    static const int32_t any = 0;
+    wkv::DeltaArgs a{};
+    a.B = B, a.T = T, a.Hk = Hk, a.H = H, a.nseq = z.nseq, a.bf16 = bf16;
+    a.offsets = packed ? &any : nullptr;  // only its being there counts
+    return a;
+}
+
+bool delta_chunked(int64_t T, const DeltaSizes &z, bool packed, bool bf16)
+{
+    return bf16 && z.n > 0 && z.nseq > 0 && (packed ? T / z.nseq : T) >= kDeltaChunkedTokens;
+}
+
+int delta_fwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t nseq, bool packed, int64_t nslots,
+                    bool slots, bool bf16, DeltaSizes *z, size_t *bytes)
+{
+    int rc = delta_sizes(B, T, Hk, H, N, nseq, packed, nslots, slots, z);
+    if (rc) return rc;
+    const wkv::DeltaArgs a = delta_shape(B, T, Hk, H, *z, packed, bf16);
+    *bytes = N == 64 && delta_chunked(T, *z, packed, bf16) ? wkv::delta_t_bytes(a) : 0;
+    return RWKV_OK;
+}
+
 int delta_entry(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const void *q, const void *k, const void *v,
                 const void *g, const void *beta, float scale, int64_t nseq, const int32_t *offsets, int64_t nslots,
-                const int32_t *slots, const float *s0, void *o, float *sT, bool bf16)
+                const int32_t *slots, const float *s0, void *o, float *sT, void *workspace, size_t wbytes, bool bf16)
 {
     tl_err[0] = 0;
     DeltaSizes z;
-    int rc = delta_sizes(B, T, Hk, H, N, nseq, offsets != nullptr, nslots, slots != nullptr, &z);
+    size_t need = 0;
+    int rc = delta_fwd_bytes(B, T, Hk, H, N, nseq, offsets != nullptr, nslots, slots != nullptr, bf16, &z, &need);
     if (rc) return rc;
     if (z.nseq == 0 || H == 0 || N == 0 || (z.n == 0 && !(sT && z.ns > 0))) return RWKV_OK;
     if (N != 64) return fail(RWKV_ERR_UNSUPPORTED, "head size N must be 64%s");
     if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(RWKV_ERR_ARG, "scale must be finite%s");
     if (z.n > 0 && (!q || !k || !v || !g || !beta || !o))
         return fail(RWKV_ERR_NULL, "q, k, v, g, beta and o must be non-null%s");
-    const void *ptrs[] = {q, k, v, g, beta, s0, o, sT};
+    if (need > 0 && !workspace) return fail(RWKV_ERR_NULL, "workspace must be non-null%s");
+    if (wbytes < need) {
+        snprintf(tl_err, sizeof(tl_err), "workspace holds %zu bytes; this call needs %zu", wbytes, need);
+        return RWKV_ERR_ARG;
+    }
+    const void *ptrs[] = {q, k, v, g, beta, s0, o, sT, workspace};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return fail(RWKV_ERR_ALIGN, "tensor pointers must be 16-byte aligned%s");
     if (!aligned4(offsets) || !aligned4(slots)) return fail(RWKV_ERR_ALIGN, "index arrays must be 4-byte aligned%s");
     const int64_t esz = bf16 ? 2 : 4;
-    const Span so{o, z.n * esz}, ss0{s0, z.ns * 4}, ssT{sT, z.ns * 4};
+    const Span so{o, z.n * esz}, ss0{s0, z.ns * 4}, ssT{sT, z.ns * 4}, sw{workspace, static_cast<int64_t>(need)};
     const Span ins[] = {{q, z.nk * esz}, {k, z.nk * esz}, {v, z.n * esz}, {g, z.nh * esz}, {beta, z.nh * esz},
                         {offsets, (z.nseq + 1) * 4}, {slots, z.nseq * 4}};
     for (const Span &x : ins) {
         if (overlap(so, x)) return fail(RWKV_ERR_ALIAS, "o overlaps an input%s");
         if (overlap(ssT, x)) return fail(RWKV_ERR_ALIAS, "sT overlaps an input%s");
+        if (overlap(sw, x)) return fail(RWKV_ERR_ALIAS, "the workspace overlaps an input%s");
     }
+    if (overlap(sw, so) || overlap(sw, ss0) || overlap(sw, ssT))
+        return fail(RWKV_ERR_ALIAS, "the workspace overlaps an output or a state%s");
     if (overlap(so, ss0) || overlap(so, ssT)) return fail(RWKV_ERR_ALIAS, "o overlaps a state%s");
     if (s0 != sT && overlap(ssT, ss0)) return fail(RWKV_ERR_ALIAS, "sT partially overlaps s0%s");
     int *status = nullptr;
     rc = status_word(&status);
     if (rc) return rc;
     const wkv::DeltaArgs a{B, T, Hk, H, z.nseq, offsets, z.nslots, slots, q, k, v, g, beta, scale, s0, o, sT, bf16, status};
-    const bool chunked = bf16 && z.n > 0 && (offsets ? T / z.nseq : T) >= kDeltaChunkedTokens;
-    const cudaError_t e = chunked ? wkv::delta_chunked_launch(a, tl_stream) : wkv::delta_recurrent_launch(a, tl_stream);
+    cudaError_t e;
+    if (need > 0) {
+        e = wkv::delta_prep_launch(a, workspace, tl_stream);
+        if (e == cudaSuccess) e = wkv::delta_chunked_launch(a, workspace, tl_stream);
+    } else {
+        e = wkv::delta_recurrent_launch(a, tl_stream);
+    }
     return e == cudaSuccess ? RWKV_OK : cuda_fail(e, "delta launch");
 }
 
@@ -400,10 +439,7 @@ int delta_bwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int6
     int64_t per, all;  // the largest workspace: a 64 x 64 fp32 state every 8 tokens and two fp32 shares
     if (!mul_ok(T / 8 + z->nseq + 2, H, &per) || !mul_ok(per, B > 0 ? B : 1, &all) || !mul_ok(all, 8192, &all))
         return fail(RWKV_ERR_SHAPE, "workspace size overflows%s");
-    wkv::DeltaArgs a{};
-    a.B = B, a.T = T, a.Hk = Hk, a.H = H, a.nseq = z->nseq, a.bf16 = bf16;
-    static const int32_t any = 0;
-    a.offsets = packed ? &any : nullptr;  // only its being there counts
+    const wkv::DeltaArgs a = delta_shape(B, T, Hk, H, *z, packed, bf16);
     *bytes = z->nseq > 0 && z->nh > 0 && N == 64 ? wkv::delta_walks_workspace_bytes(a) : 0;
     return RWKV_OK;
 }
@@ -590,17 +626,28 @@ int rwkv_wkv6_backward_omega_bf16(int64_t B, int64_t T, int64_t H, int64_t N, co
 int rwkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const float *q, const float *k,
                        const float *v, const float *g, const float *beta, float scale, int64_t nseq,
                        const int32_t *offsets, int64_t nslots, const int32_t *slots, const float *s0, float *o,
-                       float *sT)
+                       float *sT, void *workspace, size_t workspace_bytes)
 {
-    return delta_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, nslots, slots, s0, o, sT, false);
+    return delta_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, nslots, slots, s0, o, sT, workspace,
+                       workspace_bytes, false);
 }
 
 int rwkv_delta_forward_bf16(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, const uint16_t *q,
                             const uint16_t *k, const uint16_t *v, const uint16_t *g, const uint16_t *beta,
                             float scale, int64_t nseq, const int32_t *offsets, int64_t nslots, const int32_t *slots,
-                            const float *s0, uint16_t *o, float *sT)
+                            const float *s0, uint16_t *o, float *sT, void *workspace, size_t workspace_bytes)
 {
-    return delta_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, nslots, slots, s0, o, sT, true);
+    return delta_entry(B, T, Hk, H, N, q, k, v, g, beta, scale, nseq, offsets, nslots, slots, s0, o, sT, workspace,
+                       workspace_bytes, true);
+}
+
+int rwkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t nseq,
+                                       int packed, int bf16, size_t *bytes)
+{
+    tl_err[0] = 0;
+    if (!bytes) return fail(RWKV_ERR_NULL, "bytes must be non-null%s");
+    DeltaSizes z;
+    return delta_fwd_bytes(B, T, Hk, H, N, nseq, packed != 0, 0, false, bf16 != 0, &z, bytes);
 }
 
 int rwkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t nseq,

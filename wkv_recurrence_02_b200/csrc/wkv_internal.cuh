@@ -182,7 +182,12 @@ struct DeltaArgs {
     int *status;
 };
 cudaError_t delta_recurrent_launch(const DeltaArgs &a, cudaStream_t s);
-cudaError_t delta_chunked_launch(const DeltaArgs &a, cudaStream_t s);  // bf16, B * T > 0
+// Chunked kernels (bf16, B * T > 0).  The state-free matrix T of every chunk is formed first, in
+// scratch of delta_t_bytes(a) bytes.
+int64_t delta_chunks(const DeltaArgs &a);
+size_t delta_t_bytes(const DeltaArgs &a);
+cudaError_t delta_prep_launch(const DeltaArgs &a, void *t_out, cudaStream_t s);
+cudaError_t delta_chunked_launch(const DeltaArgs &a, const void *t, cudaStream_t s);
 
 // Gated delta rule backward; gradients in the type of the inputs, state gradients fp32.
 struct DeltaBwdArgs {

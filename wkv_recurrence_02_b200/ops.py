@@ -88,15 +88,16 @@ def load(path: str = LIB_PATH):
     delta = [_i64] * 5 + [_vp] * 5 + [ctypes.c_float, _i64, _vp]
     for name in ("rwkv_delta_forward", "rwkv_delta_forward_bf16"):
         fn = getattr(lib, name)
-        fn.argtypes = delta + [_i64, _vp, _vp, _vp, _vp]
+        fn.argtypes = delta + [_i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t]
         fn.restype = ctypes.c_int
     for name in ("rwkv_delta_backward", "rwkv_delta_backward_bf16"):
         fn = getattr(lib, name)
         fn.argtypes = delta + [_vp] * 10 + [ctypes.c_size_t]
         fn.restype = ctypes.c_int
-    lib.rwkv_delta_backward_workspace_bytes.argtypes = [_i64] * 6 + [ctypes.c_int, ctypes.c_int,
-                                                                     ctypes.POINTER(ctypes.c_size_t)]
-    lib.rwkv_delta_backward_workspace_bytes.restype = ctypes.c_int
+    for name in ("rwkv_delta_forward_workspace_bytes", "rwkv_delta_backward_workspace_bytes"):
+        fn = getattr(lib, name)
+        fn.argtypes = [_i64] * 6 + [ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+        fn.restype = ctypes.c_int
     lib.rwkv_state_copy.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp]
     lib.rwkv_state_copy.restype = ctypes.c_int
     lib.rwkv_state_compact.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp]
@@ -399,7 +400,20 @@ def _delta_shapes(q, k, v, g, beta, offsets):
     return B, T, Hk, H, N, nseq, dt
 
 
-def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=None, want_state=True, o=None, sT=None):
+def _delta_workspace(fn, B, T, Hk, H, N, nseq, packed, bf16):
+    out = ctypes.c_size_t(0)
+    _check(fn(B, T, Hk, H, N, nseq, packed, bf16, ctypes.byref(out)))
+    return out.value
+
+
+def delta_forward_workspace_bytes(B, T, Hk, H, N=64, nseq=None, packed=False, bf16=True) -> int:
+    """Device scratch (bytes) that a delta-rule forward call of this shape needs."""
+    return _delta_workspace(load().rwkv_delta_forward_workspace_bytes, B, T, Hk, H, N, B if nseq is None else nseq,
+                            packed, bf16)
+
+
+def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=None, want_state=True, o=None, sT=None,
+                  workspace=None):
     """Gated delta rule: S' = exp(g) S, u = beta (v - k S'), S = S' + k^T u, o = scale q S.
 
     q, k: [B,T,Hk,N] fp32|bf16; v: [B,T,H,N]; g, beta: [B,T,H] (Hk divides H).  scale: default
@@ -425,23 +439,25 @@ def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=Non
     if sT is None and want_state:
         sT = torch.empty(nseq, H, N, N, device=q.device, dtype=torch.float32)
     _cuda(sT, "sT", torch.float32, (nslots, H, N, N))
-    _same_device(q, s0=s0, slots=slots, o=o, sT=sT)
-    fn = lib.rwkv_delta_forward_bf16 if dt == torch.bfloat16 else lib.rwkv_delta_forward
+    bf = dt == torch.bfloat16
+    if workspace is None:
+        need = _delta_workspace(lib.rwkv_delta_forward_workspace_bytes, B, T, Hk, H, N, nseq, offsets is not None, bf)
+        if need:
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    _cuda(workspace, "workspace", torch.uint8)
+    _same_device(q, s0=s0, slots=slots, o=o, sT=sT, workspace=workspace)
+    fn = lib.rwkv_delta_forward_bf16 if bf else lib.rwkv_delta_forward
     with _on_device_of(lib, q):
         _check(fn(B, T, Hk, H, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                   N ** -0.5 if scale is None else float(scale), nseq, _ptr(offsets), nslots, _ptr(slots), _ptr(s0),
-                  _ptr(o), _ptr(sT)))
+                  _ptr(o), _ptr(sT), _ptr(workspace), 0 if workspace is None else workspace.numel()))
     return (o, sT) if want_state else o
 
 
 def delta_backward_workspace_bytes(B, T, Hk, H, N=64, nseq=None, packed=False, bf16=True) -> int:
     """Device scratch (bytes) that a delta-rule backward call of this shape needs."""
-    lib = load()
-    out = ctypes.c_size_t(0)
-    _check(lib.rwkv_delta_backward_workspace_bytes(int(B), int(T), int(Hk), int(H), int(N),
-                                                   int(B if nseq is None else nseq), int(packed), int(bf16),
-                                                   ctypes.byref(out)))
-    return int(out.value)
+    return _delta_workspace(load().rwkv_delta_backward_workspace_bytes, B, T, Hk, H, N, B if nseq is None else nseq,
+                            packed, bf16)
 
 
 def delta_backward(q, k, v, g, beta, do, scale=None, s0=None, dsT=None, offsets=None, want_ds0=True, workspace=None):
