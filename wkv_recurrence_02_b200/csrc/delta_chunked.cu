@@ -6,19 +6,26 @@
 // delta_prep.cu.  (Forming T here too, in the same warps, was slower: T's code and the chain's
 // together do not stay in the instruction caches, and each ran at half its speed.)  Two CTAs
 // share an SM.  Per chunk:
-//   chain group (warps 4-7)  S -> K S -> W -> T W = U -> K^T diag(tail) U -> S: three products,
-//                            each waiting for the last; beside them scale diag(gamma) Q S + P U;
-//   P group (warps 0-3)      Q K^T on the tensor core, decay ratios, P; runs ahead.
+//   chain group (warps 4-7)   S -> K S -> W -> T W = U -> K^T diag(tail) U -> S: three products,
+//                             each waiting for the last, and nothing else;
+//   output group (warps 0-3)  Q K^T and P a chunk ahead, scale diag(gamma) Q S + P U, the output;
+//   issuer (warp 8)           all products but Q K^T: issuing four takes some 150 cycles, which a
+//                             warp of the chain would be late with its share of the next step;
+//   loader (warp 9)           the copies of later chunks.
 //
 // Accuracy.  The state is an fp32 result, so every operand between S and the next S is two bf16
 // terms, hi and lo (K and V are exact): S, W, T and diag(tail) U, three products where both
 // sides are split.  What that leaves is 2^-16 of each operand.  The output is rounded to bf16,
 // and there P, U and the S of Q S are single bf16.
 //
+// A product of N = 64 takes 50 cycles of the tensor core whatever M is, one of N = 128 takes 64
+// (measured): so the two terms of an operand lie side by side as one B of 128 columns, and their
+// accumulators are added when they are read.
+//
 // Shared memory (13 tiles of 8 KB): K, Q and T (hi, lo) of two chunks, V of one (it is read early
-// in the chain), P, and three chain tiles A, B, C that take S hi/lo (A, B), W hi/lo (C, B),
-// diag(tail) U hi/lo (A, B) and U (C) in turn.  Tensor memory (256 columns): Q K^T, one accumulator
-// that takes K S, U and K^T U in turn, and the outputs of two chunks.
+// in the chain), P, and three chain tiles A, B, C in a row that take S hi/lo (A, B), W hi/lo
+// (B, C), diag(tail) U hi/lo (A, B) and U (C) in turn.  Tensor memory (256 columns): the chain's
+// accumulators (128) and, for two chunks, one that takes Q K^T and then the output.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records RWKV_ERR_TIMEOUT in the device
 // status word, waits (bounded) for its own copies and MMAs, frees its tensor memory and returns.
@@ -28,7 +35,7 @@ namespace wkv {
 namespace {
 using namespace dtc;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 320;
 constexpr int OFF_K = 0, OFF_Q = 2 * kTile, OFF_V = 4 * kTile, OFF_P = 5 * kTile, OFF_T = 6 * kTile;
 constexpr int OFF_A = 10 * kTile, OFF_B = 11 * kTile, OFF_CC = 12 * kTile;
 constexpr int OFF_PN = 13 * kTile;         // [64] sums of log2 decays inside the block: integer part
@@ -38,10 +45,10 @@ constexpr int OFF_PRE = OFF_CF + 256;      // [64] decay from the block's start 
 constexpr int OFF_BS = OFF_PRE + 256;      // [4] integer, [4] fraction parts of the blocks' sums
 constexpr int OFF_ARR = OFF_BS + 32;       // [chunk % 3][gamma, tail, beta][64]
 constexpr int OFF_BAR = OFF_ARR + 3 * 768;
-constexpr int OFF_MISC = OFF_BAR + 20 * 8;
+constexpr int OFF_MISC = OFF_BAR + 22 * 8;
 constexpr int kSmemBytes = OFF_MISC + 32 + 1024;  // + alignment slack
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
-constexpr uint32_t COL_QK = 0, COL_X = 64, COL_O = 128, kTmemCols = 256;
+constexpr uint32_t COL_X = 0, COL_O = 128, kTmemCols = 256;
 
 struct Params {
     int64_t B, T, Hk, H, nseq, nslots;
@@ -72,16 +79,19 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const uint32_t bar_q0 = smem_u32(&bars[2]);
     const uint32_t bar_t0 = smem_u32(&bars[4]);
     const uint32_t bar_v = smem_u32(&bars[6]);
-    const uint32_t bar_a = smem_u32(&bars[7]);   // Q K^T done
-    const uint32_t bar_x = smem_u32(&bars[8]);   // K S, U, K^T U done (three phases a chunk)
-    const uint32_t bar_qs = smem_u32(&bars[9]);  // Q S done
-    const uint32_t bar_o = smem_u32(&bars[10]);  // P U done
-    const uint32_t bar_p = smem_u32(&bars[11]);  // P written
-    const uint32_t bar_never = smem_u32(&bars[12]);
-    const uint32_t bar_drain = smem_u32(&bars[13]);
-    // decays written, tail rows of K and Q zeroed: + 8 * (chunk % 3), since the P group may pass
-    // two more chunks here before the chain waits for this one
-    const uint32_t bar_s0 = smem_u32(&bars[14]);
+    const uint32_t bar_a = smem_u32(&bars[7]);    // Q K^T done
+    const uint32_t bar_x = smem_u32(&bars[8]);    // K S, U, K^T U done (three phases a chunk)
+    const uint32_t bar_qs = smem_u32(&bars[9]);   // Q S done
+    const uint32_t bar_o = smem_u32(&bars[10]);   // P U done
+    const uint32_t bar_p = smem_u32(&bars[11]);   // P written, Q S scaled
+    const uint32_t bar_sr = smem_u32(&bars[12]);  // Q K^T read: its columns may take Q S
+    const uint32_t bar_tf = smem_u32(&bars[13]);  // U done: V and T have been read
+    const uint32_t bar_kf0 = smem_u32(&bars[14]); // K^T U done: K and Q have been read, + 8 * (chunk % 2)
+    const uint32_t bar_r = smem_u32(&bars[16]);   // S, W, U written (three phases a chunk)
+    const uint32_t bar_never = smem_u32(&bars[17]);
+    // decays written, tail rows of K and Q zeroed: + 8 * (chunk % 3)
+    const uint32_t bar_s0 = smem_u32(&bars[18]);
+    const uint32_t bar_drain = smem_u32(&bars[21]);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, see elect_one
@@ -97,7 +107,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const int64_t ntok = p.B * p.T;
 
     if (tid == 0) {
-        for (int i = 0; i < 17; ++i) bar_init(smem_u32(&bars[i]), i == 11 ? 128 : i == 13 ? 3 : i > 13 ? 65 : 1);
+        for (int i = 0; i < 22; ++i)
+            bar_init(smem_u32(&bars[i]), i == 11 || i == 12 || i == 16 ? 128 : i == 21 ? 2 : i > 17 ? 65 : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         misc[1] = 0;
     }
@@ -134,7 +145,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                       (8 - 2 * (col >> 1)) * 128, bar);
         }
     };
-    if (warp == 7) {
+    if (warp == 9) {
         for (int c = 0; c < 2 && c < nchunks; ++c) {
             if (elect_one()) {
                 load_tile(&map_k, OFF_K + kTile * c, hk, c, bar_k0 + 8 * c);
@@ -150,8 +161,85 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     abort = __syncthreads_or(abort);
     if (abort) misc[1] = 1;
 
-    if (warp < 4) {
-        // --------------------------------------------------------------------- P group
+    if (warp == 8) {
+        // ---------------------------------------------------------------------- issuer
+        const uint32_t tA = smem_u32(sm + OFF_A), tB = smem_u32(sm + OFF_B), tC = smem_u32(sm + OFF_CC);
+        const uint64_t dA = desc_mn(tA), dB = desc_mn(tB), dC = desc_mn(tC), dP = desc_k(smem_u32(sm + OFF_P));
+        constexpr uint32_t kId = idesc(64, 0, 1), kId2 = idesc(128, 0, 1), kIdT2 = idesc(128, 1, 1);
+        uint32_t rph = 0;
+        int ok = !abort;
+        for (int c = 0; c < nchunks && ok; ++c) {
+            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (c & 1)), aT = smem_u32(sm + OFF_T + 2 * kTile * (c & 1));
+            const uint64_t dK = desc_k(aK), dKt = desc_mn(aK), dQ = desc_k(smem_u32(sm + OFF_Q + kTile * (c & 1)));
+            const uint64_t dTh = desc_t(aT), dTl = desc_t(aT + kTile);
+            const uint32_t co = tbase + COL_O + 64 * (c & 1);
+            auto wait = [&](uint32_t bar, uint32_t phase) {
+                if (ok) ok = __all_sync(0xffffffffu, bar_wait_spin(bar, phase, spin * 64u));
+                fence_after();
+            };
+            wait(bar_s0 + 8 * (c % 3), (c / 3) & 1);
+            wait(bar_r, rph);  // S
+            rph ^= 1;
+            if (ok && elect_one()) {  // K S
+                mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, kId2);
+                mma_commit(bar_x);
+            }
+            __syncwarp();
+            wait(bar_sr, c & 1);
+            if (ok && elect_one()) {  // Q S
+                mma_tile<kStepK, kStepMn, false>(co, dQ, dA, kId);
+                mma_commit(bar_qs);
+            }
+            __syncwarp();
+            wait(bar_t0 + 8 * (c & 1), (c >> 1) & 1);
+            wait(bar_r, rph);  // W
+            rph ^= 1;
+            if (ok && elect_one()) {  // U = T W
+                mma_tile<kStepTK, kStepMn, false>(tbase + COL_X, dTh, dB, kId2);
+                mma_tile<kStepTK, kStepMn, true>(tbase + COL_X, dTl, dB, kId);
+                mma_commit(bar_x);
+                mma_commit(bar_tf);
+            }
+            __syncwarp();
+            wait(bar_r, rph);  // U
+            rph ^= 1;
+            if (ok && elect_one()) {  // K^T diag(tail) U
+                mma_tile<kStepMn, kStepMn, false>(tbase + COL_X, dKt, dA, kIdT2);
+                mma_commit(bar_x);
+                mma_commit(bar_kf0 + 8 * (c & 1));  // and Q S before it
+            }
+            __syncwarp();
+            wait(bar_p, c & 1);
+            if (ok && elect_one()) {  // + P U
+                mma_tile<kStepK, kStepMn, true>(co, dP, dC, kId);
+                mma_commit(bar_o);
+            }
+            __syncwarp();
+        }
+        if (!ok) misc[1] = 1;
+    } else if (warp == 9) {
+        // ---------------------------------------------------------------------- loader
+        // A wait by parity must not be two phases late.  The chain cannot reach U of chunk c + 1
+        // before V of c + 1, which is loaded after the wait for U of c; nor K^T U of c + 2 before
+        // K of c + 2, loaded after the wait for K^T U of c (whose barriers alternate).
+        int ok = 1;
+        for (int c = 0; c + 1 < nchunks && !abort && ok; ++c) {
+            ok = __all_sync(0xffffffffu, bar_wait(bar_tf, c & 1, spin));
+            if (!ok) break;
+            if (elect_one()) load_tile(&map_v, OFF_V, h, c + 1, bar_v);
+            __syncwarp();
+            if (c + 2 >= nchunks) break;
+            load_t(c + 2);
+            ok = __all_sync(0xffffffffu, bar_wait(bar_kf0 + 8 * (c & 1), (c >> 1) & 1, spin));
+            if (ok && elect_one()) {
+                load_tile(&map_k, OFF_K + kTile * (c & 1), hk, c + 2, bar_k0 + 8 * (c & 1));
+                load_tile(&map_q, OFF_Q + kTile * (c & 1), hk, c + 2, bar_q0 + 8 * (c & 1));
+            }
+            __syncwarp();
+        }
+        if (!ok) misc[1] = 1;
+    } else if (warp < 4) {
+        // ---------------------------------------------------------------- output group
         const int w = warp;
         float *pn = reinterpret_cast<float *>(sm + OFF_PN), *pf = reinterpret_cast<float *>(sm + OFF_PF);
         float *cf = reinterpret_cast<float *>(sm + OFF_CF), *pre = reinterpret_cast<float *>(sm + OFF_PRE);
@@ -211,15 +299,27 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             fence_after();
             const uint64_t dk = desc_k(smem_u32(kt)), dq = desc_k(smem_u32(qt));
             if (elect_one()) {
-                mma_tile<kStepK, kStepK, false>(tbase + COL_QK, dq, dk, idesc(64, 0, 0));
+                mma_tile<kStepK, kStepK, false>(tbase + COL_O + 64 * (c & 1), dq, dk, idesc(64, 0, 0));
                 mma_commit(bar_a);
                 bar_arrive(bar_s0 + 8 * (c % 3));
             }
             __syncwarp();
             return 1;
         };
-        const uint32_t qk = tbase + (static_cast<uint32_t>(32 * w) << 16) + COL_QK;
+        const uint32_t co = tbase + (static_cast<uint32_t>(32 * w) << 16) + COL_O;  // + 64 * (chunk % 2)
         const int g = lane >> 2, t = lane & 3, r0 = 16 * w + g;
+        const int row = 16 * w + (lane & 15), col = 32 * (lane >> 4);  // its output row, first of 32 columns
+        auto store_o = [&](int c) {  // output rows of chunk c
+            P2 x[16];
+            tmem_ld_row(co + 64 * (c & 1), x);
+            const int64_t tok = static_cast<int64_t>(c) * kC + row;
+            if (tok < len && in_bounds(p.status, first + tok, 1, ntok)) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((first + tok) * p.H + h) * kN + col);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[i] = make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
+            }
+        };
         int ok = 1;
         if (!abort && nchunks > 0) {
             if (w >= 2) {
@@ -236,10 +336,12 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             float x[4][2][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j <= w) tmem_ld_frag(qk + 16 * j, x[j]);
+                if (j <= w) tmem_ld_frag(co + 64 * (c & 1) + 16 * j, x[j]);
             const float n0 = pn[r0], n1 = pn[r0 + 8], f0 = pf[r0], f1 = pf[r0 + 8];
             const float p0 = p.scale * pre[r0], p1 = p.scale * pre[r0 + 8];
             tmem_wait_ld();
+            fence_before();
+            bar_arrive(bar_sr);
             uint32_t ph[4][4];  // block row w of P, bf16 pairs
             float mn = 0.f, mf = 0.f;  // decay of the whole blocks between block j and this one
 #pragma unroll
@@ -274,32 +376,50 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     }
                 }
             }
-            fence_before();
             if (named_sync_or(1, 128, !ok || misc[1])) {
                 abort = 1;
                 misc[1] = 1;
                 break;
             }
-            if (c + 1 < nchunks) {
-                if (w >= 2) scan(c + 1);
-                else if (w == 0) ok = products(c + 1);
+            if (w >= 2 && c + 1 < nchunks) scan(c + 1);
+            if (c > 0) {
+                if (ok) ok = bar_wait(bar_o, (c - 1) & 1, spin);  // P has been read, the output is there
+                fence_after();
             }
-            if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);  // the chunk before has read P
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j <= w) st_block(sm + OFF_P, w, j, lane, ph[j]);
             fence_async_smem();
+            if (c > 0) store_o(c - 1);
+            fence_before();
+            group_sync<1, 128>();
+            if (w == 0 && c + 1 < nchunks && !products(c + 1)) ok = 0;
+            // scale diag(gamma) Q S, in place
+            if (ok) ok = bar_wait(bar_qs, c & 1, spin);
+            fence_after();
+            {
+                float v[32];
+                tmem_ld32(co + 64 * (c & 1), v);
+                const float sg = p.scale * reinterpret_cast<const float *>(sm + OFF_ARR + 768 * (c % 3))[row];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= sg;
+                tmem_st32(co + 64 * (c & 1), v);
+            }
+            fence_before();
             bar_arrive(bar_p);
+        }
+        if (!abort && nchunks > 0) {
+            if (ok) ok = bar_wait(bar_o, (nchunks - 1) & 1, spin);
+            fence_after();
+            if (ok) store_o(nchunks - 1);
+            else misc[1] = 1;
         }
     } else {
         // ------------------------------------------------------------------ chain group
         const int q = warp & 3;
         const uint32_t tl = tbase + (static_cast<uint32_t>(32 * q) << 16);
-        const int row = 16 * q + (lane & 15), col = 32 * (lane >> 4);  // its row and first of 32 columns
+        const int row = 16 * q + (lane & 15), col = 32 * (lane >> 4);  // its row, first of 32 columns
         unsigned char *tA = sm + OFF_A, *tB = sm + OFF_B, *tC = sm + OFF_CC;
-        const uint64_t dA = desc_mn(smem_u32(tA)), dB = desc_mn(smem_u32(tB)), dC = desc_mn(smem_u32(tC));
-        const uint64_t dP = desc_k(smem_u32(sm + OFF_P));
-        constexpr uint32_t kIdK = idesc(64, 0, 1), kIdMn = idesc(64, 1, 1);
         const int64_t nstate = p.nslots * p.H * kN * kN;
         const int64_t sat = ((slot * p.H + h) * kN + row) * kN + col;
         P2 S[16];
@@ -318,177 +438,89 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         uint32_t at[4];  // this thread's 32 columns of a tile
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = swz(row, 2 * col + 16 * i);
-        auto store_split = [&](const P2 (&x)[16], unsigned char *th, unsigned char *tlo) {
+        // half of them (16 columns) as two bf16 terms
+        auto store_split = [&](const P2 *x, int half, unsigned char *th, unsigned char *tlo) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 uint32_t a[4], b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split2(x[4 * i + e], &a[e], &b[e]);
-                *reinterpret_cast<uint4 *>(th + at[i]) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4 *>(tlo + at[i]) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4 *>(th + at[2 * half + i]) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4 *>(tlo + at[2 * half + i]) = make_uint4(b[0], b[1], b[2], b[3]);
             }
         };
-        auto rounded = [&](const P2 (&x)[16], int i) {
-            return make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
-        };
-        // group barrier: what was written is ready for the products issued next.  Whether to stop
-        // is voted on once a chunk (an expired wait makes the rest of its chunk's waits pass).
-        auto meet = [&]() {
+        // what was written is ready for the issuer, what was read may be written again
+        auto ready = [&]() {
             fence_async_smem();
             fence_before();
-            group_sync<2, 128>();
-            fence_after();
+            bar_arrive(bar_r);
         };
-        auto vote = [&](int ok) -> bool {
-            fence_async_smem();
-            fence_before();
-            const bool stop = named_sync_or(2, 128, !ok || misc[1]);
-            fence_after();
-            return stop;
-        };
-        auto store_o = [&](int c) {  // output rows of chunk c from tensor memory
-            P2 x[16];
-            tmem_ld_row(tl + COL_O + 64 * (c & 1), x);
-            const int64_t t = static_cast<int64_t>(c) * kC + row;
-            if (t < len && in_bounds(p.status, first + t, 1, ntok)) {
-                uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((first + t) * p.H + h) * kN + col);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dst[i] = rounded(x, i);
-            }
-        };
-
-        int ok = 1;
         uint32_t xph = 0;  // phase of bar_x
-        for (int c = 0; c < nchunks && !abort; ++c) {
-            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (c & 1)), co = COL_O + 64 * (c & 1);
-            // ---- S hi, lo; K S and Q S
-            store_split(S, tA, tB);
-            if (ok) ok = bar_wait(bar_s0 + 8 * (c % 3), (c / 3) & 1, spin);
-            if (vote(ok)) {
-                abort = 1;
-                break;
-            }
-            if (warp == 4) {
-                const uint64_t dK = desc_k(aK);
-                if (elect_one()) {
-                    mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, kIdK);
-                    mma_tile<kStepK, kStepMn, true>(tbase + COL_X, dK, dB, kIdK);
-                    mma_commit(bar_x);
-                }
-                __syncwarp();
-            } else if (warp == 5) {
-                const uint64_t dQ = desc_k(smem_u32(sm + OFF_Q + kTile * (c & 1)));
-                if (elect_one()) {
-                    mma_tile<kStepK, kStepMn, false>(tbase + co, dQ, dA, kIdK);
-                    mma_commit(bar_qs);
-                }
-                __syncwarp();
-            }
+        int ok = !abort;
+        for (int c = 0; c < nchunks; ++c) {
+            if (!__all_sync(0xffffffffu, ok)) break;  // a wait ran out
+            // ---- S hi, lo
+            store_split(S, 0, tA, tB);
+            store_split(S + 8, 1, tA, tB);
+            ready();
+            // ---- W = beta (v - gamma K S)
+            ok = bar_wait(bar_s0 + 8 * (c % 3), (c / 3) & 1, spin);
             const float *arr = reinterpret_cast<const float *>(sm + OFF_ARR + 768 * (c % 3));
             const float gam = arr[row], tail = arr[64 + row], bet = arr[128 + row], gC = arr[kC - 1];
-            if (c > 0) {  // the output of the chunk before, under K S
-                if (ok) ok = bar_wait(bar_o, (c - 1) & 1, spin);
-                fence_after();
-                store_o(c - 1);
-            }
-            // ---- W = beta (v - gamma K S)
-            P2 x[16];
+            const P2 b2 = pk(bet, bet), bg = pk(-bet * gam, -bet * gam), t2 = pk(tail, tail), g2 = pk(gC, gC);
             if (ok) ok = bar_wait(bar_v, c & 1, spin);
+            if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);  // P U has read U
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
-            tmem_ld_row(tl + COL_X, x);
-            {
-                const P2 b2 = pk(bet, bet), bg = pk(-bet * gam, -bet * gam);
-                const bool token = static_cast<int64_t>(c) * kC + row < len;  // else another sequence's, or nothing
+            const bool token = static_cast<int64_t>(c) * kC + row < len;  // else another sequence's, or nothing
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+            for (int half = 0; half < 2; ++half) {
+                P2 x[8];
+                tmem_ld_sum16(tl + COL_X + 16 * half, x);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
                     uint4 vv = make_uint4(0u, 0u, 0u, 0u);
-                    if (token) vv = *reinterpret_cast<const uint4 *>(sm + OFF_V + at[i]);
+                    if (token) vv = *reinterpret_cast<const uint4 *>(sm + OFF_V + at[2 * half + i]);
                     const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[4 * i + e] = fma2(bg, x[4 * i + e], mul2(b2, unpack2(vw[e])));
                 }
-                store_split(x, tC, tB);
+                store_split(x, half, tB, tC);
             }
-            if (ok) ok = bar_wait(bar_t0 + 8 * (c & 1), (c >> 1) & 1, spin);
-            meet();
-            if (warp == 4) {  // ---- U = T W
-                const uint64_t dTh = desc_t(smem_u32(sm + OFF_T + kTile * (2 * (c & 1))));
-                const uint64_t dTl = desc_t(smem_u32(sm + OFF_T + kTile * (2 * (c & 1) + 1)));
-                if (elect_one()) {
-                    mma_tile<kStepTK, kStepMn, false>(tbase + COL_X, dTh, dC, kIdK);
-                    mma_tile<kStepTK, kStepMn, true>(tbase + COL_X, dTl, dC, kIdK);
-                    mma_tile<kStepTK, kStepMn, true>(tbase + COL_X, dTh, dB, kIdK);
-                    mma_commit(bar_x);
-                }
-                __syncwarp();
-            } else if (warp == 7 && c + 1 < nchunks) {
-                if (elect_one()) load_tile(&map_v, OFF_V, h, c + 1, bar_v);
-                __syncwarp();
-            }
-            // ---- scale diag(gamma) Q S in place, under T W
-            if (ok) ok = bar_wait(bar_qs, c & 1, spin);
-            fence_after();
-            {
-                float v[32];
-                tmem_ld32(tl + co, v);
-                const float sg = p.scale * gam;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= sg;
-                tmem_st32(tl + co, v);
-            }
+            ready();
             // ---- U, and diag(tail) U hi, lo
+            if (ok) ok = bar_wait(bar_qs, c & 1, spin);  // Q S has read S
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
-            tmem_ld_row(tl + COL_X, x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(tC + at[i]) = rounded(x, i);
+            for (int half = 0; half < 2; ++half) {
+                P2 x[8];
+                tmem_ld_sum16(tl + COL_X + 16 * half, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = mul2(x[i], pk(tail, tail));
-            store_split(x, tA, tB);
-            // P is there, and so Q K^T has read its tiles; asked before P U is issued, since the P
-            // group may then go on to the next phase of this barrier
-            if (ok && (warp == 5 || warp == 7)) ok = bar_wait(bar_p, c & 1, spin);
-            meet();
-            if (warp == 4) {  // ---- K^T diag(tail) U
-                const uint64_t dKt = desc_mn(aK);
-                if (elect_one()) {
-                    mma_tile<kStepMn, kStepMn, false>(tbase + COL_X, dKt, dA, kIdMn);
-                    mma_tile<kStepMn, kStepMn, true>(tbase + COL_X, dKt, dB, kIdMn);
-                    mma_commit(bar_x);
-                }
-                __syncwarp();
-            } else if (warp == 5) {  // ---- + P U
-                if (elect_one()) {
-                    mma_tile<kStepK, kStepMn, true>(tbase + co, dP, dC, kIdK);
-                    mma_commit(bar_o);
-                }
-                __syncwarp();
-            } else if (warp == 7 && c + 2 < nchunks) {
-                if (elect_one()) load_tile(&map_q, OFF_Q + kTile * (c & 1), hk, c + 2, bar_q0 + 8 * (c & 1));
-                __syncwarp();
-                load_t(c + 2);
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4 *>(tC + at[2 * half + i]) =
+                        make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], t2);
+                store_split(x, half, tA, tB);
             }
+            ready();
+            // ---- S
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
-            tmem_ld_row(tl + COL_X, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = fma2(pk(gC, gC), S[i], x[i]);
-            if (warp == 7 && c + 2 < nchunks) {
-                if (elect_one()) load_tile(&map_k, OFF_K + kTile * (c & 1), hk, c + 2, bar_k0 + 8 * (c & 1));
-                __syncwarp();
+            for (int half = 0; half < 2; ++half) {
+                P2 x[8];
+                tmem_ld_sum16(tl + COL_X + 16 * half, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) S[8 * half + i] = fma2(g2, S[8 * half + i], x[i]);
             }
         }
-        if (!abort && nchunks > 0) {
-            if (ok) ok = bar_wait(bar_o, (nchunks - 1) & 1, spin);
-            if (vote(ok)) abort = 1;
-            else store_o(nchunks - 1);
-        }
-        if (abort) misc[1] = 1;
-        if (!abort && p.sT && slot >= 0 && in_bounds(p.status, sat, 32, nstate)) {
+        if (!ok) misc[1] = 1;
+        if (ok && p.sT && slot >= 0 && in_bounds(p.status, sat, 32, nstate)) {
             float4 *dst = reinterpret_cast<float4 *>(p.sT + sat);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dst[i] = make_float4(lo(S[2 * i]), hi(S[2 * i]), lo(S[2 * i + 1]), hi(S[2 * i + 1]));
@@ -501,7 +533,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     fence_after();
     if (abort) {
         record_status(p.status, kStatusTimeout);
-        if ((warp == 0 || warp == 4 || warp == 5) && elect_one()) mma_commit(bar_drain);  // the three issuers
+        if ((warp == 0 || warp == 8) && elect_one()) mma_commit(bar_drain);  // the two issuers
         if (tid == 0) {
             bar_wait(bar_drain, 0, p.spin_limit);
             for (int i = 0; i < 7; ++i)  // copies in flight: a barrier that nothing will complete runs out

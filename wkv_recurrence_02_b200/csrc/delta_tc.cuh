@@ -100,6 +100,28 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][4])
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// Two accumulators, 64 columns apart, added: threads 0-15 hold columns c .. c + 15, threads 16-31
+// c + 32 .. c + 47, each thread one lane, as pairs.
+__device__ __forceinline__ void tmem_ld_sum16(uint32_t taddr, P2 (&x)[8])
+{
+    uint32_t a[16], b[16];
+#define WKV_LD16(r, at)                                                                                              \
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "                                                         \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 32;"                               \
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),   \
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),          \
+                   "=r"(r[15])                                                                                       \
+                 : "r"(at))
+    WKV_LD16(a, taddr);
+    WKV_LD16(b, taddr + 64);
+#undef WKV_LD16
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = add2(pk(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])),
+                    pk(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1])));
+}
+
 // 16 TMEM lanes x 64 columns: threads 0-15 hold columns 0-31, threads 16-31 32-63, each thread one
 // lane, as pairs.
 __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, P2 (&x)[16])
