@@ -277,18 +277,27 @@ template <typename T> cudaError_t launch(const DeltaBwdArgs &a, cudaStream_t s)
         static_cast<T *>(a.dq), static_cast<T *>(a.dk), static_cast<T *>(a.dv), static_cast<T *>(a.dg),
         static_cast<T *>(a.dbeta));
     e = cudaGetLastError();
-    if (e == cudaSuccess && share && ntok > 0) {
-        const int64_t blocks = (ntok * f.Hk * kN + 255) / 256;
-        if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        delta_sum_heads_kernel<T><<<static_cast<unsigned>(blocks), 256, 0, s>>>(
-            ntok, f.Hk, f.H, f.nseq, f.offsets, share, share + ntok * f.H * kN, static_cast<T *>(a.dq),
-            static_cast<T *>(a.dk));
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && share) e = delta_sum_heads_launch(a, share, share + ntok * f.H * kN, s);
     return e;
 }
 
 }  // namespace
+
+cudaError_t delta_sum_heads_launch(const DeltaBwdArgs &a, const float *dq_h, const float *dk_h, cudaStream_t s)
+{
+    const DeltaArgs &f = a.f;
+    const int64_t ntok = f.B * f.T, blocks = (ntok * f.Hk * kN + 255) / 256;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (f.bf16)
+        delta_sum_heads_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(
+            ntok, f.Hk, f.H, f.nseq, f.offsets, dq_h, dk_h, static_cast<__nv_bfloat16 *>(a.dq),
+            static_cast<__nv_bfloat16 *>(a.dk));
+    else
+        delta_sum_heads_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(
+            ntok, f.Hk, f.H, f.nseq, f.offsets, dq_h, dk_h, static_cast<float *>(a.dq), static_cast<float *>(a.dk));
+    return cudaGetLastError();
+}
 
 size_t delta_walks_workspace_bytes(const DeltaArgs &a)
 {

@@ -1,0 +1,885 @@
+// delta_backward_tc.cu -- gradients of the gated delta rule on B200 tensor cores, bf16 inputs.
+//
+// delta_tc.cuh has the chunk's forward algebra (T, P, U, gamma, tail).  Reversed, with dS the
+// gradient of the state after the chunk and dO that of its outputs:
+//   dU = P^T dO + diag(tail) K dS            dW = T^T dU (the whole gradient of u)
+//   dS_prev = gamma_63 dS + Q^T diag(scale gamma) dO - K^T diag(beta gamma) dW
+//   A1[t][i] = scale Gamma[t][i] dO_t.U_i (i <= t)      A2[t][i] = -beta_t Gamma[t][i] dW_t.U_i (i < t)
+//   dQ = scale diag(gamma) dO S_prev^T + A1 K
+//   dK = diag(tail) U dS^T - diag(beta gamma) dW S_prev^T + A1^T Q + (A2 + A2^T) K
+//   dV = diag(beta) dW
+//   dbeta_t = dW_t.V_t - x_t,  x_t = gamma_t K_t.(dW S_prev^T)_t + sum_{i<t} Gamma[t][i] (k_t.k_i) dW_t.U_i
+//   dg_t = sum_{j>=t} e_j + sum_{i<t} tail_i K_i.(U dS^T)_i + gamma_63 <dS, S_prev>,
+//   e_t = Q_t.dQ'_t - K_t.dK'_t - 2 beta_t x_t
+// where dQ' and dK' leave out what no decay stands before: the diagonal of A1 and, in dK, diag(tail)
+// U dS^T (it enters through the second sum).  Every pair of tokens i < j of the chunk enters e_j with
+// one sign and e_i with the other, formed from the same rounded operands, and what is left out keeps
+// fast decays (whose dg is far below the other gradients) out of the rounding of slow terms.
+//
+// Four kernels: T of all chunks (delta_prep.cu); the forward walk for S_prev and U of every chunk
+// (delta_chunked.cu); delta_bwd_state_kernel, the walk back for dS and dW; delta_bwd_grad_kernel, all
+// chunks at once, for the gradients.  S_prev, U, dS and dW pass between them in bf16, as images of
+// their swizzled tiles.  ds0 is an fp32 result: between dS and dS_prev every operand is two bf16
+// terms, as the state's are in the forward walk.
+//
+// Every mbarrier wait is bounded; on expiry the CTA records RWKV_ERR_TIMEOUT in the device
+// status word, waits (bounded) for its own copies and MMAs, frees its tensor memory and returns.
+#include "delta_tc.cuh"
+
+namespace wkv {
+namespace {
+using namespace dtc;
+
+// ------------------------------------------------------------------------ the walk back
+// As the forward walk (two CTAs per SM, the same groups and the same hand-overs):
+//   chain group (warps 4-7)  dS -> K dS -> dU -> T^T dU = dW -> K^T diag(-beta gamma) dW -> dS
+//   side group (warps 0-3)   what the chain adds but does not wait for: Q K^T, P, P^T dO, and
+//                            Q^T diag(scale gamma) dO, where the chain's last product accumulates
+//   issuer (warp 8), loader (warp 9)
+constexpr int kThreads = 320;
+// 13 tiles: K, Q and dO of two chunks, T (hi, lo), a pair for P hi/lo and then diag(scale gamma) dO
+// hi/lo, and the chain's A, B, C: dS hi/lo (A, B), dU hi/lo (B, C), diag(-beta gamma) dW hi/lo (A, B)
+// and dW (C)
+constexpr int OFF_K = 0, OFF_Q = 2 * kTile, OFF_DO = 4 * kTile, OFF_T = 6 * kTile, OFF_PG = 8 * kTile;
+constexpr int OFF_A = 10 * kTile, OFF_B = 11 * kTile, OFF_CC = 12 * kTile;
+constexpr int OFF_DEC = 13 * kTile;
+constexpr int OFF_ARR = OFF_DEC + static_cast<int>(sizeof(Decays));
+constexpr int OFF_BAR = OFF_ARR + 3 * static_cast<int>(sizeof(ChunkArrays));
+constexpr int OFF_MISC = OFF_BAR + 26 * 8;
+constexpr int kSmemBytes = OFF_MISC + 32 + 1024;  // + alignment slack
+static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
+// the chain's accumulators (128); Q K^T and then P^T dO; the sum that becomes dS_prev
+constexpr uint32_t COL_X = 0, COL_R = 128, COL_Y = 192, kTmemCols = 256;
+
+struct StateParams {
+    int64_t B, T, Hk, H, nseq;
+    const int32_t *offsets;
+    const __nv_bfloat16 *g, *beta;
+    const unsigned char *t;     // [chunks][H][kTBytes]
+    int64_t nchunks;
+    float scale;
+    const float *dsT;
+    float *ds0;
+    unsigned char *ds, *dw;     // [chunks][H] tiles: dS after the chunk, dW
+    int *status;
+    uint32_t spin_limit;
+};
+
+__global__ void __launch_bounds__(kThreads, 2)
+delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_do, const StateParams p)
+{
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + OFF_MISC);  // TMEM base, abort
+    // chunks are counted as they are walked: n = 0 is the last chunk of the sequence
+    const uint32_t bar_k0 = smem_u32(&bars[0]);    // K, Q, dO there: + 8 * (n % 2)
+    const uint32_t bar_q0 = smem_u32(&bars[2]);
+    const uint32_t bar_g0 = smem_u32(&bars[4]);
+    const uint32_t bar_t = smem_u32(&bars[6]);     // T there
+    const uint32_t bar_a = smem_u32(&bars[7]);     // Q K^T done
+    const uint32_t bar_x = smem_u32(&bars[8]);     // K dS, dW, the new dS done (three phases a chunk)
+    const uint32_t bar_d0 = smem_u32(&bars[9]);    // P^T dO done
+    const uint32_t bar_y = smem_u32(&bars[10]);    // Q^T diag(scale gamma) dO done
+    const uint32_t bar_rr = smem_u32(&bars[11]);   // P^T dO read: its columns may take Q K^T
+    const uint32_t bar_yr = smem_u32(&bars[12]);   // the new dS read: its columns may be written
+    const uint32_t bar_tf = smem_u32(&bars[13]);   // T has been read
+    const uint32_t bar_kf0 = smem_u32(&bars[14]);  // K, Q, dO have been read: + 8 * (n % 2)
+    const uint32_t bar_r = smem_u32(&bars[16]);    // dS, dU, dW written (three phases a chunk)
+    const uint32_t bar_as = smem_u32(&bars[17]);   // the copies of dS, of dW have read them
+    const uint32_t bar_cs = smem_u32(&bars[18]);
+    // decays written, tail rows zeroed: + 8 * (n % 3), since the side group may pass two more
+    // chunks here before the chain waits for this one
+    const uint32_t bar_s0 = smem_u32(&bars[19]);
+    const uint32_t bar_drain = smem_u32(&bars[22]);
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, see elect_one
+    const int64_t blk = blockIdx.x, seq = blk / p.H, h = blk % p.H, hk = h / (p.H / p.Hk);
+    int64_t first, len;
+    sequence_span(p.offsets, seq, p.T, &first, &len);
+    const int nchunks = static_cast<int>((len + kC - 1) / kC);
+    const int64_t chunk0 = first_chunk(p.offsets != nullptr, seq, first, p.T);
+    const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = p.offsets ? static_cast<int>(first) : 0;
+    const uint32_t spin = p.spin_limit;
+    const int64_t ntok = p.B * p.T;
+
+    if (tid == 0) {
+        for (int i = 0; i < 23; ++i)
+            bar_init(smem_u32(&bars[i]), i == 11 || i == 12 || i == 16 ? 128 : i == 22 ? 2 : i >= 19 ? 65 : 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        misc[1] = 0;
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(const_cast<uint32_t *>(misc))),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    for (int i = tid; i < 2 * kTile / 16; i += kThreads)  // T: the blocks above the diagonal, once
+        *reinterpret_cast<uint4 *>(sm + OFF_T + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tbase = misc[0];
+
+    auto load_tile = [&](const CUtensorMap *map, uint32_t off, int64_t head, int n, uint32_t bar) {
+        const int c = nchunks - 1 - n;
+        if (!tma_coord_ok(p.status, 0, 2, kN, row_t + static_cast<int64_t>(c) * kC, p.T)) return;
+        bar_expect_tx(bar, kTile);
+        tma_load_4d(smem_u32(sm + off), map, 0, static_cast<int>(head), row_t + c * kC, row_b, bar);
+    };
+    auto load_tiles = [&](int n) {  // K, Q, dO: one thread
+        load_tile(&map_k, OFF_K + kTile * (n & 1), hk, n, bar_k0 + 8 * (n & 1));
+        load_tile(&map_q, OFF_Q + kTile * (n & 1), hk, n, bar_q0 + 8 * (n & 1));
+        load_tile(&map_do, OFF_DO + kTile * (n & 1), h, n, bar_g0 + 8 * (n & 1));
+    };
+    auto load_t = [&](int n) {  // one warp, a copy for each of 8 core columns of each term
+        const int64_t id = chunk0 + nchunks - 1 - n;
+        if (!in_bounds(p.status, id, 1, p.nchunks)) return;
+        if (lane == 0) bar_expect_tx(bar_t, kTBytes);
+        __syncwarp();
+        if (lane < 16) {
+            const int col = lane & 7, term = lane >> 3;
+            bulk_load(smem_u32(sm + OFF_T + kTile * term + 1024 * col + 256 * (col >> 1)),
+                      p.t + (id * p.H + h) * kTBytes + term * kTStored + t_stored_at(col), (8 - 2 * (col >> 1)) * 128,
+                      bar_t);
+        }
+    };
+
+    int ok = 1;
+    if (warp == 9) {
+        // ---------------------------------------------------------------------- loader
+        // No wait by parity can be two phases late: dW of n + 1 needs the T loaded after the wait
+        // for dW of n; the new dS of n + 2 the K loaded after the wait for that of n (whose barriers
+        // alternate).
+        for (int n = 0; n < 2 && n < nchunks; ++n) {
+            if (elect_one()) load_tiles(n);
+            __syncwarp();
+        }
+        if (nchunks > 0) load_t(0);
+        for (int n = 0; n + 1 < nchunks && ok; ++n) {
+            ok = __all_sync(0xffffffffu, bar_wait(bar_tf, n & 1, spin));
+            if (!ok) break;
+            load_t(n + 1);
+            if (n + 2 >= nchunks) break;
+            ok = __all_sync(0xffffffffu, bar_wait(bar_kf0 + 8 * (n & 1), (n >> 1) & 1, spin));
+            if (ok && elect_one()) load_tiles(n + 2);
+            __syncwarp();
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------------- issuer
+        const uint32_t tA = smem_u32(sm + OFF_A), tB = smem_u32(sm + OFF_B), tC = smem_u32(sm + OFF_CC);
+        const uint64_t dA = desc_mn(tA), dB = desc_mn(tB);
+        const uint64_t dTh = desc_tt(smem_u32(sm + OFF_T)), dTl = desc_tt(smem_u32(sm + OFF_T + kTile));
+        uint32_t rph = 0;
+        auto wait = [&](uint32_t bar, uint32_t phase) {
+            if (ok) ok = __all_sync(0xffffffffu, bar_wait_spin(bar, phase, spin * 64u));
+            fence_after();
+        };
+        for (int n = 0; n < nchunks && ok; ++n) {
+            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (n & 1));
+            const uint64_t dK = desc_k(aK), dKt = desc_mn(aK);
+            const int64_t id = chunk0 + nchunks - 1 - n, tile = (id * p.H + h) * kTile;
+            wait(bar_s0 + 8 * (n % 3), (n / 3) & 1);
+            wait(bar_r, rph);  // dS
+            rph ^= 1;
+            if (ok && lane == 0 && in_bounds(p.status, id, 1, p.nchunks)) {
+                bulk_store(p.ds + tile, tA, kTile);
+                bulk_commit();
+            }
+            if (ok && elect_one()) {  // K dS
+                mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, idesc(128, 0, 1));
+                mma_commit(bar_x);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                bulk_wait_read<0>();
+                bar_arrive(bar_as);
+            }
+            wait(bar_t, n & 1);
+            wait(bar_r, rph);  // dU
+            rph ^= 1;
+            if (ok && elect_one()) {  // dW = T^T dU
+                mma_tile<kStepTMn, kStepMn, false>(tbase + COL_X, dTh, dB, idesc(128, 1, 1));
+                mma_tile<kStepTMn, kStepMn, true>(tbase + COL_X, dTl, dB, idesc(64, 1, 1));
+                mma_commit(bar_x);
+                mma_commit(bar_tf);
+            }
+            __syncwarp();
+            wait(bar_y, n & 1);
+            wait(bar_r, rph);  // dW
+            rph ^= 1;
+            if (ok && lane == 0 && in_bounds(p.status, id, 1, p.nchunks)) {
+                bulk_store(p.dw + tile, tC, kTile);
+                bulk_commit();
+            }
+            if (ok && elect_one()) {  // + K^T diag(-beta gamma) dW
+                mma_tile<kStepMn, kStepMn, true>(tbase + COL_Y, dKt, dA, idesc(64, 1, 1));
+                mma_tile<kStepMn, kStepMn, true>(tbase + COL_Y, dKt, dB, idesc(64, 1, 1));
+                mma_commit(bar_x);
+                mma_commit(bar_kf0 + 8 * (n & 1));  // Q and dO: read before bar_y
+            }
+            __syncwarp();
+            if (lane == 0) {
+                bulk_wait_read<0>();
+                bar_arrive(bar_cs);
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+    } else if (warp < 4) {
+        // ------------------------------------------------------------------ side group
+        const int w = warp;
+        Decays &dec = *reinterpret_cast<Decays *>(sm + OFF_DEC);
+        ChunkArrays *arrays = reinterpret_cast<ChunkArrays *>(sm + OFF_ARR);
+        const int st = tid - 64;
+        uint16_t g_next = 0, b_next = 0;
+        auto fetch = [&](int n) {  // g and beta of a token, a chunk ahead
+            const int64_t t = static_cast<int64_t>(nchunks - 1 - n) * kC + st;
+            g_next = b_next = 0;
+            if (t >= len || !in_bounds(p.status, first + t, 1, ntok)) return;
+            const int64_t at = (first + t) * p.H + h;
+            g_next = reinterpret_cast<const uint16_t *>(p.g)[at];
+            b_next = reinterpret_cast<const uint16_t *>(p.beta)[at];
+        };
+        auto scan = [&](int n) {
+            const float gv = widen(g_next), bv = widen(b_next);
+            if (n + 1 < nchunks) fetch(n + 1);
+            scan_decays<3>(dec, arrays[n % 3], st, gv, bv);
+            bar_arrive(bar_s0 + 8 * (n % 3));
+        };
+        auto products = [&](int n) -> int {  // Q K^T (warp 0)
+            unsigned char *kt = sm + OFF_K + kTile * (n & 1), *qt = sm + OFF_Q + kTile * (n & 1), *gt = sm + OFF_DO + kTile * (n & 1);
+            const uint32_t ph = (n >> 1) & 1;
+            const bool there = bar_wait(bar_k0 + 8 * (n & 1), ph, spin) && bar_wait(bar_q0 + 8 * (n & 1), ph, spin) &&
+                               bar_wait(bar_g0 + 8 * (n & 1), ph, spin) &&
+                               (n == 0 || bar_wait(bar_rr, (n - 1) & 1, spin));
+            if (!__all_sync(0xffffffffu, there)) return 0;
+            const int tv = static_cast<int>(len - static_cast<int64_t>(nchunks - 1 - n) * kC);
+            if (tv < kC) {
+                zero_rows(kt, tv, lane, 32);
+                zero_rows(qt, tv, lane, 32);
+                zero_rows(gt, tv, lane, 32);
+                fence_async_smem();
+                __syncwarp();
+            }
+            fence_after();
+            const uint64_t dk = desc_k(smem_u32(kt)), dq = desc_k(smem_u32(qt));
+            if (elect_one()) {
+                mma_tile<kStepK, kStepK, false>(tbase + COL_R, dq, dk, idesc(64, 0, 0));
+                mma_commit(bar_a);
+                bar_arrive(bar_s0 + 8 * (n % 3));
+            }
+            __syncwarp();
+            return 1;
+        };
+        const uint32_t qk = tbase + (static_cast<uint32_t>(32 * w) << 16) + COL_R;
+        const int row = 16 * w + (lane & 15), col = 32 * (lane >> 4);
+        unsigned char *ph_t = sm + OFF_PG, *pl_t = sm + OFF_PG + kTile;
+        int abort = 0;
+        if (nchunks > 0) {
+            if (w >= 2) {
+                fetch(0);
+                scan(0);
+            } else if (w == 0) {
+                ok = products(0);
+            }
+        }
+        for (int n = 0; n < nchunks && !abort; ++n) {
+            group_sync<1, 128>();  // the chunk's decays are there
+            if (ok) ok = bar_wait(bar_a, n & 1, spin);
+            fence_after();
+            uint32_t ph[4][4], pl[4][4];
+            form_p<true>(dec, w, lane, qk, p.scale, ph, pl, [] {});
+            fence_before();
+            if (named_sync_or(1, 128, !ok || misc[1])) {
+                abort = 1;
+                misc[1] = 1;
+                break;
+            }
+            if (w >= 2 && n + 1 < nchunks) scan(n + 1);
+            // ---- P^T dO; the pair of tiles was last read by the product that bar_y stands for
+            if (ok && n > 0) ok = bar_wait(bar_y, (n - 1) & 1, spin);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                st_block(ph_t, w, j, lane, ph[j]);
+                st_block(pl_t, w, j, lane, pl[j]);
+            }
+            fence_async_smem();
+            group_sync<1, 128>();
+            const unsigned char *gt = sm + OFF_DO + kTile * (n & 1);
+            if (w == 0) {
+                fence_after();
+                const uint64_t dp = desc_mn(smem_u32(ph_t)), dl = desc_mn(smem_u32(pl_t)), dg = desc_mn(smem_u32(gt));
+                if (elect_one()) {
+                    mma_tile<kStepMn, kStepMn, false>(tbase + COL_R, dp, dg, idesc(64, 1, 1));
+                    mma_tile<kStepMn, kStepMn, true>(tbase + COL_R, dl, dg, idesc(64, 1, 1));
+                    mma_commit(bar_d0);
+                }
+                __syncwarp();
+            }
+            // ---- diag(scale gamma) dO hi, lo, then its product with Q^T
+            const float sg = p.scale * arrays[n % 3].gamma[row];
+            if (ok) ok = bar_wait(bar_g0 + 8 * (n & 1), (n >> 1) & 1, spin);
+            uint32_t xh[4][4], xl[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 y = *reinterpret_cast<const uint4 *>(gt + swz(row, 2 * col + 16 * i));
+                const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split2(mul2(unpack2(yw[e]), pk(sg, sg)), &xh[i][e], &xl[i][e]);
+            }
+            if (ok) ok = bar_wait(bar_d0, n & 1, spin);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at = swz(row, 2 * col + 16 * i);
+                *reinterpret_cast<uint4 *>(ph_t + at) = make_uint4(xh[i][0], xh[i][1], xh[i][2], xh[i][3]);
+                *reinterpret_cast<uint4 *>(pl_t + at) = make_uint4(xl[i][0], xl[i][1], xl[i][2], xl[i][3]);
+            }
+            fence_async_smem();
+            group_sync<1, 128>();
+            if (w == 0) {
+                if (n > 0 && ok) ok = __all_sync(0xffffffffu, bar_wait(bar_yr, (n - 1) & 1, spin));
+                fence_after();
+                const uint64_t dq = desc_mn(smem_u32(sm + OFF_Q + kTile * (n & 1)));
+                const uint64_t dh = desc_mn(smem_u32(ph_t)), dl = desc_mn(smem_u32(pl_t));
+                if (elect_one()) {
+                    mma_tile<kStepMn, kStepMn, false>(tbase + COL_Y, dq, dh, idesc(64, 1, 1));
+                    mma_tile<kStepMn, kStepMn, true>(tbase + COL_Y, dq, dl, idesc(64, 1, 1));
+                    mma_commit(bar_y);
+                }
+                __syncwarp();
+                if (n + 1 < nchunks && !products(n + 1)) ok = 0;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------ chain group
+        const int q = warp & 3;
+        const uint32_t tl = tbase + (static_cast<uint32_t>(32 * q) << 16);
+        const int row = 16 * q + (lane & 15), col = 32 * (lane >> 4);  // its row, first of 32 columns
+        unsigned char *tA = sm + OFF_A, *tB = sm + OFF_B, *tC = sm + OFF_CC;
+        const int64_t sat = ((seq * p.H + h) * kN + row) * kN + col, nstate = p.nseq * p.H * kN * kN;
+        P2 S[16];
+        if (p.dsT && in_bounds(p.status, sat, 32, nstate)) {
+            const float4 *src = reinterpret_cast<const float4 *>(p.dsT + sat);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 x = src[i];
+                S[2 * i] = pk(x.x, x.y);
+                S[2 * i + 1] = pk(x.z, x.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = pk(0.f, 0.f);
+        }
+        uint32_t at[4];  // this thread's 32 columns of a tile
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = swz(row, 2 * col + 16 * i);
+        auto store_split = [&](const P2 *x, int half, unsigned char *th, unsigned char *tlo) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split2(x[4 * i + e], &a[e], &b[e]);
+                *reinterpret_cast<uint4 *>(th + at[2 * half + i]) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4 *>(tlo + at[2 * half + i]) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+        };
+        auto ready = [&]() {
+            fence_async_smem();
+            fence_before();
+            bar_arrive(bar_r);
+        };
+        uint32_t xph = 0;  // phase of bar_x
+        for (int n = 0; n < nchunks; ++n) {
+            if (!__all_sync(0xffffffffu, ok)) break;  // a wait ran out
+            // ---- dS hi, lo
+            store_split(S, 0, tA, tB);
+            store_split(S + 8, 1, tA, tB);
+            ready();
+            // ---- dU = P^T dO + diag(tail) K dS
+            ok = bar_wait(bar_s0 + 8 * (n % 3), (n / 3) & 1, spin);
+            const ChunkArrays &arr = reinterpret_cast<const ChunkArrays *>(sm + OFF_ARR)[n % 3];
+            const float bg = -arr.beta[row] * arr.gamma[row], tail = arr.tail[row], gC = arr.gamma[kC - 1];
+            if (ok) ok = bar_wait(bar_d0, n & 1, spin);
+            if (ok && n > 0) ok = bar_wait(bar_cs, (n - 1) & 1, spin);
+            if (ok) ok = bar_wait(bar_x, xph, spin);
+            xph ^= 1;
+            fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                P2 x[8];
+                tmem_ld_sum16(tl + COL_X + 16 * half, x);
+                float d0[16];
+                tmem_ld16(tl + COL_R + 16 * half, d0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fma2(pk(tail, tail), x[i], pk(d0[2 * i], d0[2 * i + 1]));
+                store_split(x, half, tB, tC);
+            }
+            fence_before();
+            bar_arrive(bar_rr);
+            ready();
+            // ---- dW, and diag(-beta gamma) dW hi, lo
+            if (ok) ok = bar_wait(bar_as, n & 1, spin);
+            if (ok) ok = bar_wait(bar_x, xph, spin);
+            xph ^= 1;
+            fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                P2 x[8];
+                tmem_ld_sum16(tl + COL_X + 16 * half, x);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4 *>(tC + at[2 * half + i]) =
+                        make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], pk(bg, bg));
+                store_split(x, half, tA, tB);
+            }
+            ready();
+            // ---- dS
+            if (ok) ok = bar_wait(bar_x, xph, spin);
+            xph ^= 1;
+            fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float y[16];
+                tmem_ld16(tl + COL_Y + 16 * half, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    S[8 * half + i] = fma2(pk(gC, gC), S[8 * half + i], pk(y[2 * i], y[2 * i + 1]));
+            }
+            fence_before();
+            bar_arrive(bar_yr);
+        }
+        if (ok && p.ds0 && in_bounds(p.status, sat, 32, nstate)) {
+            float4 *dst = reinterpret_cast<float4 *>(p.ds0 + sat);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(lo(S[2 * i]), hi(S[2 * i]), lo(S[2 * i + 1]), hi(S[2 * i + 1]));
+        }
+    }
+    if (!ok) misc[1] = 1;
+
+    // ---- drain after an abort, then release tensor memory
+    fence_before();
+    const int abort = __syncthreads_or(misc[1] != 0);
+    fence_after();
+    if (abort) {
+        record_status(p.status, kStatusTimeout);
+        if ((warp == 0 || warp == 8) && elect_one()) mma_commit(bar_drain);  // the two issuers
+        if (tid == 0) {
+            bar_wait(bar_drain, 0, p.spin_limit);
+            for (int i = 0; i < 7; ++i)  // copies in flight: a barrier that nothing will complete runs out
+                for (uint32_t ph = 0; ph < 2; ++ph) bar_wait(smem_u32(&bars[i]), ph, 200);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols));
+}
+
+// ----------------------------------------------------------------------- gradients of a chunk
+// One block of eight warps per (chunk, value head), two per SM: warp (q, half) holds rows
+// 16 q .. 16 q + 15 and 32 of the 64 columns.  Eight tiles: what the walks left (U and S_prev side
+// by side: dW [U | S_prev]^T is one product of N = 128), Q, K, dO, and A1; A2 goes where dW was
+// (each thread overwrites what only it reads), diag(scale gamma) dO where dO was.
+constexpr int kGThreads = 256;
+constexpr int GO_Q = 0, GO_K = kTile, GO_DO = 2 * kTile, GO_U = 3 * kTile, GO_S = 4 * kTile, GO_DW = 5 * kTile;
+constexpr int GO_DS = 6 * kTile, GO_A1 = 7 * kTile, GO_DEC = 8 * kTile;
+constexpr int GO_ARR = GO_DEC + static_cast<int>(sizeof(Decays));
+constexpr int GO_RED = GO_ARR + static_cast<int>(sizeof(ChunkArrays));  // [4 sums][2 halves][64], [8] warps' sums, [4]
+constexpr int GO_DIAG = GO_RED + 4 * 2 * 256 + 64;  // [64] diagonal of A1
+constexpr int GO_BAR = GO_DIAG + 256;
+constexpr int kGSmemBytes = GO_BAR + 32 + 1024;
+constexpr uint32_t GC_DOU = 0, GC_DWU = 64, GC_DWS = 128, GC_KK = 192;     // first products
+constexpr uint32_t GC_DQ = GC_DOU, GC_DK = GC_DWU, GC_UDS = GC_KK;         // second ones
+
+struct GradParams {
+    int64_t B, T, Hk, H, nseq;
+    const int32_t *offsets;
+    const __nv_bfloat16 *v, *g, *beta;
+    float scale;
+    const unsigned char *states, *us, *ds, *dw;  // [chunks][H] tiles
+    int64_t nchunks;
+    __nv_bfloat16 *dq, *dk, *dv, *dg, *dbeta;
+    float *dq_h, *dk_h;  // [B,T,H,64] shares of the value heads, or null
+    int *status;
+    uint32_t spin_limit;
+};
+
+// 16 of 32 columns of this thread's row: threads 0-15 columns c .. c + 15, threads 16-31 the next 16.
+__device__ __forceinline__ void tmem_ld_part(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15])
+                 : "r"(taddr));
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 bf16 of a swizzled tile's row
+__device__ __forceinline__ void ld_row16(const unsigned char *tile, int row, int col, float (&x)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 y = *reinterpret_cast<const uint4 *>(tile + swz(row, 2 * col + 16 * i));
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+            x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+    }
+}
+__device__ __forceinline__ void st_global16(__nv_bfloat16 *p, const float (&x)[16])
+{
+    uint4 *dst = reinterpret_cast<uint4 *>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                            pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+}
+__device__ __forceinline__ void st_global16(float *p, const float (&x)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+
+__global__ void __launch_bounds__(kGThreads, 2)
+delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_do, const GradParams p)
+{
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int64_t h = blockIdx.x % p.H, id = blockIdx.x / p.H, hk = h / (p.H / p.Hk);
+    int64_t seq, first, len;
+    const int64_t c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
+    if (c < 0) return;  // a number that no chunk has
+    const int64_t t0 = first + c * kC, ntok = p.B * p.T;
+    const int tv = static_cast<int>(len - c * kC < kC ? len - c * kC : kC);
+    const uint32_t bar0 = smem_u32(sm + GO_BAR), bar1 = bar0 + 8, bar2 = bar0 + 16;
+    volatile uint32_t *tm = reinterpret_cast<volatile uint32_t *>(sm + GO_BAR + 24);
+    Decays &dec = *reinterpret_cast<Decays *>(sm + GO_DEC);
+    ChunkArrays &arr = *reinterpret_cast<ChunkArrays *>(sm + GO_ARR);
+    float *red = reinterpret_cast<float *>(sm + GO_RED), *diag = reinterpret_cast<float *>(sm + GO_DIAG);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int i = 0; i < 3; ++i) bar_init(bar0 + 8 * i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = static_cast<int>(p.offsets ? t0 : c * kC);
+            const int64_t tile = (id * p.H + h) * kTile;
+            if (tma_coord_ok(p.status, 0, 2, kN, row_t, p.T) && in_bounds(p.status, id, 1, p.nchunks)) {
+                bar_expect_tx(bar0, 7 * kTile);
+                tma_load_4d(smem_u32(sm + GO_Q), &map_q, 0, static_cast<int>(hk), row_t, row_b, bar0);
+                tma_load_4d(smem_u32(sm + GO_K), &map_k, 0, static_cast<int>(hk), row_t, row_b, bar0);
+                tma_load_4d(smem_u32(sm + GO_DO), &map_do, 0, static_cast<int>(h), row_t, row_b, bar0);
+                bulk_load(smem_u32(sm + GO_U), p.us + tile, kTile, bar0);
+                bulk_load(smem_u32(sm + GO_S), p.states + tile, kTile, bar0);
+                bulk_load(smem_u32(sm + GO_DW), p.dw + tile, kTile, bar0);
+                bulk_load(smem_u32(sm + GO_DS), p.ds + tile, kTile, bar0);
+            }
+        }
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(const_cast<uint32_t *>(tm))),
+                     "r"(256u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else if (warp < 3) {
+        const int t = tid - 32;
+        float g = 0.f, b = 0.f;
+        if (t < tv && in_bounds(p.status, t0 + t, 1, ntok)) {
+            g = __bfloat162float(p.g[(t0 + t) * p.H + h]);
+            b = __bfloat162float(p.beta[(t0 + t) * p.H + h]);
+        }
+        scan_decays<1>(dec, arr, t, g, b);
+    }
+    // this thread's row and its 16 columns; v of that place comes straight from global memory
+    const int q = warp & 3, half = warp >> 2, row = 16 * q + (lane & 15), blk = 2 * half + (lane >> 4), col = 16 * blk;
+    const int64_t token = t0 + row, at = (token * p.H + h) * kN + col;
+    const bool valid = row < tv && in_bounds(p.status, token, 1, ntok);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    if (valid) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 y = reinterpret_cast<const uint4 *>(p.v + at)[i];
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+                v[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tbase = tm[0], tl = tbase + (static_cast<uint32_t>(32 * q) << 16) + 32 * half;
+    int ok = bar_wait(bar0, 0, p.spin_limit);
+    if (tv < kC) {
+        zero_rows(sm + GO_Q, tv, tid, kGThreads);
+        zero_rows(sm + GO_K, tv, tid, kGThreads);
+        zero_rows(sm + GO_DO, tv, tid, kGThreads);
+        fence_async_smem();
+    }
+    const bool go = !__syncthreads_or(!ok);
+    if (go) {
+        const uint32_t aQ = smem_u32(sm + GO_Q), aK = smem_u32(sm + GO_K), aO = smem_u32(sm + GO_DO);
+        const uint32_t aU = smem_u32(sm + GO_U), aS = smem_u32(sm + GO_S), aW = smem_u32(sm + GO_DW);
+        const uint32_t aD = smem_u32(sm + GO_DS), a1 = smem_u32(sm + GO_A1);
+        if (warp == 0) {
+            const uint64_t dO = desc_k(aO), dU = desc_k(aU), dW = desc_k(aW), dK = desc_k(aK);
+            if (elect_one()) {
+                mma_tile<kStepK, kStepK, false>(tbase + GC_DOU, dO, dU, idesc(64, 0, 0));
+                mma_tile<kStepK, kStepK, false>(tbase + GC_DWU, dW, dU, idesc(128, 0, 0));  // dW U^T, dW S_prev^T
+                mma_tile<kStepK, kStepK, false>(tbase + GC_KK, dK, dK, idesc(64, 0, 0));
+                mma_commit(bar1);
+            }
+            __syncwarp();
+        }
+        const float beta = arr.beta[row], gam = arr.gamma[row], tail = arr.tail[row];
+        // ---- dV and the row's dW.V; <dS, S_prev>
+        float dots = 0.f, dwv = 0.f;
+        {
+            float x[16], y[16];
+            ld_row16(sm + GO_DW, row, col, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                dwv = fmaf(x[i], v[i], dwv);
+                x[i] *= beta;
+            }
+            if (valid) st_global16(p.dv + at, x);
+            ld_row16(sm + GO_S, row, col, x);
+            ld_row16(sm + GO_DS, row, col, y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dots = fmaf(x[i], y[i], dots);
+        }
+        ok = bar_wait(bar1, 0, p.spin_limit);
+        fence_after();
+        // ---- A1, A2 and x = gamma K.(dW S_prev^T) + sum Gamma (k k) (dW.U)
+        float xt = 0.f, kr[16];
+        ld_row16(sm + GO_K, row, col, kr);
+        {
+            float s[16];
+            tmem_ld_part(tl + GC_DWS, s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) xt = fmaf(kr[i], s[i], xt);
+            xt *= gam;
+        }
+        {
+            float o[16], wu[16], kk[16];
+            tmem_ld_part(tl + GC_DOU, o);
+            tmem_ld_part(tl + GC_DWU, wu);
+            tmem_ld_part(tl + GC_KK, kk);
+            const float n0 = dec.pn[row], f0 = dec.pf[row];
+            float mn = 0.f, mf = 0.f;
+#pragma unroll
+            for (int m = 1; m < 3; ++m)
+                if (m > blk && m < q) mn += dec.bs[m], mf += dec.bs[4 + m];
+            const float rf = ex2_approx((n0 + mn) + (f0 + mf));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float gm = 0.f;
+                if (blk < q) gm = rf * dec.cf[col + i];
+                else if (blk == q && i <= (lane & 15)) gm = ex2_approx((n0 - dec.pn[col + i]) + (f0 - dec.pf[col + i]));
+                o[i] *= p.scale * gm;
+                if (blk == q && i == (lane & 15)) {  // A1's diagonal is added to dQ and dK at the end
+                    diag[row] = o[i];
+                    o[i] = gm = 0.f;
+                }
+                const float gw = gm * wu[i];
+                xt = fmaf(gw, kk[i], xt);
+                wu[i] = -beta * gw;
+            }
+            st_row16_bf16(sm + GO_A1, row, 2 * col, o);
+            st_row16_bf16(sm + GO_DW, row, 2 * col, wu);
+        }
+        {
+            float x[16];
+            const float sg = p.scale * gam;
+            ld_row16(sm + GO_DO, row, col, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] *= sg;
+            st_row16_bf16(sm + GO_DO, row, 2 * col, x);
+        }
+        fence_async_smem();
+        fence_before();
+        ok = !__syncthreads_or(!ok);
+        fence_after();
+        if (warp == 0 && ok) {
+            const uint64_t dO = desc_k(aO), dS = desc_k(aS), dA1 = desc_k(a1), dA1t = desc_mn(a1), dA2 = desc_k(aW), dA2t = desc_mn(aW);
+            const uint64_t dKn = desc_mn(aK), dQn = desc_mn(aQ), dU = desc_k(aU), dD = desc_k(aD);
+            if (elect_one()) {
+                mma_tile<kStepK, kStepK, false>(tbase + GC_DQ, dO, dS, idesc(64, 0, 0));
+                mma_tile<kStepK, kStepMn, true>(tbase + GC_DQ, dA1, dKn, idesc(64, 0, 1));
+                mma_tile<kStepK, kStepMn, false>(tbase + GC_DK, dA2, dKn, idesc(64, 0, 1));
+                mma_tile<kStepMn, kStepMn, true>(tbase + GC_DK, dA2t, dKn, idesc(64, 1, 1));
+                mma_tile<kStepMn, kStepMn, true>(tbase + GC_DK, dA1t, dQn, idesc(64, 1, 1));
+                mma_tile<kStepK, kStepK, false>(tbase + GC_UDS, dU, dD, idesc(64, 0, 0));
+                mma_commit(bar2);
+            }
+            __syncwarp();
+        }
+        float e = 0.f, r2 = 0.f;
+        if (ok) ok = bar_wait(bar2, 0, p.spin_limit);
+        fence_after();
+        {
+            const float a = diag[row], bg = -beta * gam;
+            float x[16], y[16], z[16], qr[16];
+            tmem_ld_part(tl + GC_DQ, x);
+            ld_row16(sm + GO_Q, row, col, qr);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                e = fmaf(x[i], qr[i], e);
+                x[i] = fmaf(a, kr[i], x[i]);
+            }
+            if (valid) {
+                if (p.dq_h) st_global16(p.dq_h + at, x);
+                else st_global16(p.dq + at, x);
+            }
+            tmem_ld_part(tl + GC_DK, x);
+            tmem_ld_part(tl + GC_DWS, y);
+            tmem_ld_part(tl + GC_UDS, z);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i] = fmaf(bg, y[i], x[i]);
+                e = fmaf(-kr[i], x[i], e);
+                z[i] *= tail;
+                r2 = fmaf(kr[i], z[i], r2);
+                x[i] += fmaf(a, qr[i], z[i]);
+            }
+            if (valid) {
+                if (p.dk_h) st_global16(p.dk_h + at, x);
+                else st_global16(p.dk + at, x);
+            }
+        }
+        // ---- sums over a row's four threads, and over the chunk
+        dwv += __shfl_xor_sync(0xffffffffu, dwv, 16);
+        xt += __shfl_xor_sync(0xffffffffu, xt, 16);
+        e += __shfl_xor_sync(0xffffffffu, e, 16);
+        r2 += __shfl_xor_sync(0xffffffffu, r2, 16);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) dots += __shfl_xor_sync(0xffffffffu, dots, d);
+        if (lane < 16) {
+            red[half * 64 + row] = dwv;
+            red[128 + half * 64 + row] = xt;
+            red[256 + half * 64 + row] = e;
+            red[384 + half * 64 + row] = r2;
+        }
+        if (lane == 0) red[512 + warp] = dots;
+        __syncthreads();
+        if (warp < 2) {
+            const int t = tid;
+            const float x = red[128 + t] + red[192 + t], own = red[384 + t] + red[448 + t];
+            float s = red[256 + t] + red[320 + t] - 2.f * arr.beta[t] * x, before = own;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {  // from the token to its warp's last; from the first to the token
+                const float y = __shfl_down_sync(0xffffffffu, s, d), z = __shfl_up_sync(0xffffffffu, before, d);
+                if (lane + d < 32) s += y;
+                if (lane >= d) before += z;
+            }
+            if (lane == 0) red[520 + warp] = s;
+            if (lane == 31) red[522 + warp] = before;
+            before = __shfl_up_sync(0xffffffffu, before, 1);  // without the token itself
+            if (lane == 0) before = 0.f;
+            group_sync<1, 64>();
+            if (warp == 0) s += red[521];
+            else before += red[522];
+            float dot = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) dot += red[512 + w];
+            if (t < tv && in_bounds(p.status, t0 + t, 1, ntok)) {
+                p.dg[(t0 + t) * p.H + h] = __float2bfloat16_rn(s + (before + arr.gamma[kC - 1] * dot));
+                p.dbeta[(t0 + t) * p.H + h] = __float2bfloat16_rn(red[t] + red[64 + t] - x);
+            }
+        }
+    }
+    fence_before();
+    const int bad = __syncthreads_or(!go || !ok);
+    fence_after();
+    if (bad && tid == 0) {
+        record_status(p.status, kStatusTimeout);
+        for (int i = 0; i < 3; ++i) bar_wait(bar0 + 8 * i, 0, 200);  // what is in flight
+    }
+    __syncthreads();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(256u));
+}
+
+// Byte layout of the workspace: T, four tiles for every chunk and value head, the value heads'
+// shares of dq and dk.
+struct Layout {
+    size_t t, states, us, ds, dw, shares, total;
+};
+Layout layout(const DeltaArgs &a)
+{
+    const size_t tiles = static_cast<size_t>(delta_chunks(a) * a.H) * kTile;
+    Layout l;
+    l.t = 0;
+    l.states = (delta_t_bytes(a) + 1023) / 1024 * 1024;
+    l.us = l.states + tiles;
+    l.ds = l.us + tiles;
+    l.dw = l.ds + tiles;
+    l.shares = l.dw + tiles;
+    l.total = l.shares + (a.H == a.Hk ? 0 : static_cast<size_t>(2 * a.B * a.T * a.H * kN) * sizeof(float));
+    return l;
+}
+
+}  // namespace
+
+size_t delta_backward_tc_workspace_bytes(const DeltaArgs &a) { return layout(a).total; }
+
+cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s)
+{
+    const DeltaArgs &f = a.f;
+    if (f.nseq * f.H == 0) return cudaSuccess;
+    const int64_t chunks = delta_chunks(f);
+    if (chunks * f.H > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const Layout l = layout(f);
+    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+    CUtensorMap mq, mk, mo;
+    if (!make_map(&mq, f.q, f.B, f.T, f.Hk) || !make_map(&mk, f.k, f.B, f.T, f.Hk) || !make_map(&mo, a.dout, f.B, f.T, f.H))
+        return cudaErrorInvalidValue;
+    cudaError_t e = delta_prep_launch(f, ws + l.t, s);
+    if (e != cudaSuccess) return e;
+    e = delta_states_launch(f, ws + l.t, ws + l.states, ws + l.us, s);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(delta_bwd_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_bwd_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmemBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_bwd_state_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_bwd_grad_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(f.g), *beta = static_cast<const __nv_bfloat16 *>(f.beta);
+    const StateParams sp{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, g, beta, ws + l.t, chunks, f.scale, a.dsT, a.ds0,
+                         ws + l.ds, ws + l.dw, f.status, 100000u};
+    delta_bwd_state_kernel<<<static_cast<unsigned>(f.nseq * f.H), kThreads, kSmemBytes, s>>>(mq, mk, mo, sp);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const bool shared = f.H != f.Hk;
+    float *dq_h = shared ? reinterpret_cast<float *>(ws + l.shares) : nullptr;
+    float *dk_h = shared ? dq_h + f.B * f.T * f.H * kN : nullptr;
+    const GradParams gp{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, static_cast<const __nv_bfloat16 *>(f.v), g, beta, f.scale,
+                        ws + l.states, ws + l.us, ws + l.ds, ws + l.dw, chunks,
+                        static_cast<__nv_bfloat16 *>(a.dq), static_cast<__nv_bfloat16 *>(a.dk),
+                        static_cast<__nv_bfloat16 *>(a.dv), static_cast<__nv_bfloat16 *>(a.dg),
+                        static_cast<__nv_bfloat16 *>(a.dbeta), dq_h, dk_h, f.status, 100000u};
+    delta_bwd_grad_kernel<<<static_cast<unsigned>(chunks * f.H), kGThreads, kGSmemBytes, s>>>(mq, mk, mo, gp);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && shared) e = delta_sum_heads_launch(a, dq_h, dk_h, s);
+    return e;
+}
+
+}  // namespace wkv

@@ -27,6 +27,9 @@
 // (B, C), diag(tail) U hi/lo (A, B) and U (C) in turn.  Tensor memory (256 columns): the chain's
 // accumulators (128) and, for two chunks, one that takes Q K^T and then the output.
 //
+// The backward pass's first walk is the same kernel (STATES): without queries and outputs, it
+// leaves the bf16 state before every chunk and U, as images of their tiles.
+//
 // Every mbarrier wait is bounded; on expiry the CTA records RWKV_ERR_TIMEOUT in the device
 // status word, waits (bounded) for its own copies and MMAs, frees its tensor memory and returns.
 #include "delta_tc.cuh"
@@ -38,13 +41,9 @@ using namespace dtc;
 constexpr int kThreads = 320;
 constexpr int OFF_K = 0, OFF_Q = 2 * kTile, OFF_V = 4 * kTile, OFF_P = 5 * kTile, OFF_T = 6 * kTile;
 constexpr int OFF_A = 10 * kTile, OFF_B = 11 * kTile, OFF_CC = 12 * kTile;
-constexpr int OFF_PN = 13 * kTile;         // [64] sums of log2 decays inside the block: integer part
-constexpr int OFF_PF = OFF_PN + 256;       // [64] fraction part
-constexpr int OFF_CF = OFF_PF + 256;       // [64] decay from after the token to its block's end
-constexpr int OFF_PRE = OFF_CF + 256;      // [64] decay from the block's start up to the token
-constexpr int OFF_BS = OFF_PRE + 256;      // [4] integer, [4] fraction parts of the blocks' sums
-constexpr int OFF_ARR = OFF_BS + 32;       // [chunk % 3][gamma, tail, beta][64]
-constexpr int OFF_BAR = OFF_ARR + 3 * 768;
+constexpr int OFF_DEC = 13 * kTile;                               // Decays
+constexpr int OFF_ARR = OFF_DEC + static_cast<int>(sizeof(Decays));  // ChunkArrays, [chunk % 3]
+constexpr int OFF_BAR = OFF_ARR + 3 * static_cast<int>(sizeof(ChunkArrays));
 constexpr int OFF_MISC = OFF_BAR + 22 * 8;
 constexpr int kSmemBytes = OFF_MISC + 32 + 1024;  // + alignment slack
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
@@ -60,11 +59,13 @@ struct Params {
     const float *s0;
     __nv_bfloat16 *o;
     float *sT;
+    unsigned char *states, *us;  // STATES: [chunks][H] tiles of 8 KB
     int *status;
     uint32_t spin_limit;
     int inject_timeout;
 };
 
+template <bool STATES>
 __global__ void __launch_bounds__(kThreads, 2)
 delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const Params p)
@@ -149,7 +150,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         for (int c = 0; c < 2 && c < nchunks; ++c) {
             if (elect_one()) {
                 load_tile(&map_k, OFF_K + kTile * c, hk, c, bar_k0 + 8 * c);
-                load_tile(&map_q, OFF_Q + kTile * c, hk, c, bar_q0 + 8 * c);
+                if (!STATES) load_tile(&map_q, OFF_Q + kTile * c, hk, c, bar_q0 + 8 * c);
                 if (c < 1) load_tile(&map_v, OFF_V, h, c, bar_v);
             }
             __syncwarp();
@@ -180,13 +181,22 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             wait(bar_s0 + 8 * (c % 3), (c / 3) & 1);
             wait(bar_r, rph);  // S
             rph ^= 1;
+            const int64_t tile = ((chunk0 + c) * p.H + h) * kTile;
+            if (STATES && ok && lane == 0 && in_bounds(p.status, chunk0 + c, 1, p.nchunks)) {
+                bulk_store(p.states + tile, tA, kTile);
+                bulk_commit();
+            }
             if (ok && elect_one()) {  // K S
                 mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, kId2);
                 mma_commit(bar_x);
             }
             __syncwarp();
-            wait(bar_sr, c & 1);
-            if (ok && elect_one()) {  // Q S
+            if (!STATES) wait(bar_sr, c & 1);
+            if (STATES && lane == 0) {  // the copy of S has read it
+                bulk_wait_read<0>();
+                bar_arrive(bar_qs);
+            }
+            if (!STATES && ok && elect_one()) {  // Q S
                 mma_tile<kStepK, kStepMn, false>(co, dQ, dA, kId);
                 mma_commit(bar_qs);
             }
@@ -203,19 +213,28 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             __syncwarp();
             wait(bar_r, rph);  // U
             rph ^= 1;
+            if (STATES && ok && lane == 0 && in_bounds(p.status, chunk0 + c, 1, p.nchunks)) {
+                bulk_store(p.us + tile, tC, kTile);
+                bulk_commit();
+            }
             if (ok && elect_one()) {  // K^T diag(tail) U
                 mma_tile<kStepMn, kStepMn, false>(tbase + COL_X, dKt, dA, kIdT2);
                 mma_commit(bar_x);
                 mma_commit(bar_kf0 + 8 * (c & 1));  // and Q S before it
             }
             __syncwarp();
-            wait(bar_p, c & 1);
-            if (ok && elect_one()) {  // + P U
+            if (!STATES) wait(bar_p, c & 1);
+            if (STATES && lane == 0) {  // the copy of U has read it
+                bulk_wait_read<0>();
+                bar_arrive(bar_o);
+            }
+            if (!STATES && ok && elect_one()) {  // + P U
                 mma_tile<kStepK, kStepMn, true>(co, dP, dC, kId);
                 mma_commit(bar_o);
             }
             __syncwarp();
         }
+        if (STATES && lane == 0) bulk_wait_all();
         if (!ok) misc[1] = 1;
     } else if (warp == 9) {
         // ---------------------------------------------------------------------- loader
@@ -233,7 +252,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             ok = __all_sync(0xffffffffu, bar_wait(bar_kf0 + 8 * (c & 1), (c >> 1) & 1, spin));
             if (ok && elect_one()) {
                 load_tile(&map_k, OFF_K + kTile * (c & 1), hk, c + 2, bar_k0 + 8 * (c & 1));
-                load_tile(&map_q, OFF_Q + kTile * (c & 1), hk, c + 2, bar_q0 + 8 * (c & 1));
+                if (!STATES) load_tile(&map_q, OFF_Q + kTile * (c & 1), hk, c + 2, bar_q0 + 8 * (c & 1));
             }
             __syncwarp();
         }
@@ -241,9 +260,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     } else if (warp < 4) {
         // ---------------------------------------------------------------- output group
         const int w = warp;
-        float *pn = reinterpret_cast<float *>(sm + OFF_PN), *pf = reinterpret_cast<float *>(sm + OFF_PF);
-        float *cf = reinterpret_cast<float *>(sm + OFF_CF), *pre = reinterpret_cast<float *>(sm + OFF_PRE);
-        float *bs = reinterpret_cast<float *>(sm + OFF_BS);
+        Decays &dec = *reinterpret_cast<Decays *>(sm + OFF_DEC);
+        ChunkArrays *arrays = reinterpret_cast<ChunkArrays *>(sm + OFF_ARR);
         // Warps 2 and 3 prepare the decays; the tokens' g and beta are loaded a chunk ahead and
         // widened only when their chunk comes, so that nothing waits for the load before.
         const int st = tid - 64;
@@ -257,44 +275,27 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             b_next = reinterpret_cast<const uint16_t *>(p.beta)[at];
         };
         auto scan = [&](int c) {
-            const float gv = __uint_as_float(static_cast<uint32_t>(g_next) << 16);
-            const float bv = __uint_as_float(static_cast<uint32_t>(b_next) << 16);
+            const float gv = widen(g_next), bv = widen(b_next);
             if (c + 1 < nchunks) fetch(c + 1);
-            float *out = reinterpret_cast<float *>(sm + OFF_ARR + 768 * (c % 3));
-            const int wb = st >> 4;
-            const BlockSums s = block_sums(gv, st);
-            pn[st] = s.n;
-            pf[st] = s.f;
-            cf[st] = ex2_approx((s.bn - s.n) + (s.bf - s.f));
-            pre[st] = ex2_approx(s.n + s.f);
-            out[128 + st] = bv;
-            if ((st & 15) == 15) {
-                bs[wb] = s.n;
-                bs[4 + wb] = s.f;
-            }
-            group_sync<3, 64>();
-            float gn = s.n, gf = s.f, tn = s.bn - s.n, tf = s.bf - s.f;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if (m < wb) gn += bs[m], gf += bs[4 + m];
-                if (m > wb) tn += bs[m], tf += bs[4 + m];
-            }
-            out[st] = ex2_approx(gn + gf);
-            out[64 + st] = ex2_approx(tn + tf);
+            scan_decays<3>(dec, arrays[c % 3], st, gv, bv);
             bar_arrive(bar_s0 + 8 * (c % 3));
         };
         // Q K^T of chunk c (warp 0)
         auto products = [&](int c) -> int {
             unsigned char *kt = sm + OFF_K + kTile * (c & 1), *qt = sm + OFF_Q + kTile * (c & 1);
             const bool there = bar_wait(bar_k0 + 8 * (c & 1), (c >> 1) & 1, spin) &&
-                               bar_wait(bar_q0 + 8 * (c & 1), (c >> 1) & 1, spin);
+                               (STATES || bar_wait(bar_q0 + 8 * (c & 1), (c >> 1) & 1, spin));
             if (!__all_sync(0xffffffffu, there)) return 0;
             const int64_t left = len - static_cast<int64_t>(c) * kC;
             if (left < kC) {
                 zero_rows(kt, static_cast<int>(left), lane, 32);
-                zero_rows(qt, static_cast<int>(left), lane, 32);
+                if (!STATES) zero_rows(qt, static_cast<int>(left), lane, 32);
                 fence_async_smem();
                 __syncwarp();
+            }
+            if (STATES) {
+                if (lane == 0) bar_arrive(bar_s0 + 8 * (c % 3));
+                return 1;
             }
             fence_after();
             const uint64_t dk = desc_k(smem_u32(kt)), dq = desc_k(smem_u32(qt));
@@ -307,7 +308,6 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             return 1;
         };
         const uint32_t co = tbase + (static_cast<uint32_t>(32 * w) << 16) + COL_O;  // + 64 * (chunk % 2)
-        const int g = lane >> 2, t = lane & 3, r0 = 16 * w + g;
         const int row = 16 * w + (lane & 15), col = 32 * (lane >> 4);  // its output row, first of 32 columns
         auto store_o = [&](int c) {  // output rows of chunk c
             P2 x[16];
@@ -331,51 +331,26 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         for (int c = 0; c < nchunks && !abort; ++c) {
             group_sync<1, 128>();  // the chunk's decays are there
+            if (STATES) {  // nothing but the next chunk's decays and tail rows
+                if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);
+                if (named_sync_or(1, 128, !ok || misc[1])) {
+                    abort = 1;
+                    misc[1] = 1;
+                    break;
+                }
+                if (c + 1 < nchunks) {
+                    if (w >= 2) scan(c + 1);
+                    else if (w == 0) ok = products(c + 1);
+                }
+                continue;
+            }
             if (ok) ok = bar_wait(bar_a, c & 1, spin);
             fence_after();
-            float x[4][2][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j <= w) tmem_ld_frag(co + 64 * (c & 1) + 16 * j, x[j]);
-            const float n0 = pn[r0], n1 = pn[r0 + 8], f0 = pf[r0], f1 = pf[r0 + 8];
-            const float p0 = p.scale * pre[r0], p1 = p.scale * pre[r0 + 8];
-            tmem_wait_ld();
-            fence_before();
-            bar_arrive(bar_sr);
-            uint32_t ph[4][4];  // block row w of P, bf16 pairs
-            float mn = 0.f, mf = 0.f;  // decay of the whole blocks between block j and this one
-#pragma unroll
-            for (int j = 3; j >= 0; --j) {
-                if (j > w) continue;
-                if (j == w) {
-#pragma unroll
-                    for (int nn = 0; nn < 2; ++nn) {
-                        const float2 cn = *reinterpret_cast<const float2 *>(pn + 16 * j + 8 * nn + 2 * t);
-                        const float2 ff = *reinterpret_cast<const float2 *>(pf + 16 * j + 8 * nn + 2 * t);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int col = 8 * nn + 2 * t, row = g + 8 * r;
-                            const float e0 = ex2_approx(((r ? n1 : n0) - cn.x) + ((r ? f1 : f0) - ff.x));
-                            const float e1 = ex2_approx(((r ? n1 : n0) - cn.y) + ((r ? f1 : f0) - ff.y));
-                            ph[j][2 * nn + r] = pack_bf16(col <= row ? p.scale * e0 * x[j][nn][2 * r] : 0.f,
-                                                          col + 1 <= row ? p.scale * e1 * x[j][nn][2 * r + 1] : 0.f);
-                        }
-                    }
-                    continue;
-                }
-                const float mid = ex2_approx(mn + mf);
-                mn += bs[j];
-                mf += bs[4 + j];
-#pragma unroll
-                for (int nn = 0; nn < 2; ++nn) {
-                    const P2 cc = ld_p2(cf + 16 * j + 8 * nn + 2 * t);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float f = mid * (r ? p1 : p0);
-                        ph[j][2 * nn + r] = pack2(mul2(mul2(cc, pk(f, f)), pk(x[j][nn][2 * r], x[j][nn][2 * r + 1])));
-                    }
-                }
-            }
+            uint32_t ph[4][4], pl[4][4];
+            form_p<false>(dec, w, lane, co + 64 * (c & 1), p.scale, ph, pl, [&] {
+                fence_before();
+                bar_arrive(bar_sr);
+            });
             if (named_sync_or(1, 128, !ok || misc[1])) {
                 abort = 1;
                 misc[1] = 1;
@@ -400,7 +375,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             {
                 float v[32];
                 tmem_ld32(co + 64 * (c & 1), v);
-                const float sg = p.scale * reinterpret_cast<const float *>(sm + OFF_ARR + 768 * (c % 3))[row];
+                const float sg = p.scale * arrays[c % 3].gamma[row];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= sg;
                 tmem_st32(co + 64 * (c & 1), v);
@@ -408,7 +383,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             fence_before();
             bar_arrive(bar_p);
         }
-        if (!abort && nchunks > 0) {
+        if (!STATES && !abort && nchunks > 0) {
             if (ok) ok = bar_wait(bar_o, (nchunks - 1) & 1, spin);
             fence_after();
             if (ok) store_o(nchunks - 1);
@@ -465,8 +440,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             ready();
             // ---- W = beta (v - gamma K S)
             ok = bar_wait(bar_s0 + 8 * (c % 3), (c / 3) & 1, spin);
-            const float *arr = reinterpret_cast<const float *>(sm + OFF_ARR + 768 * (c % 3));
-            const float gam = arr[row], tail = arr[64 + row], bet = arr[128 + row], gC = arr[kC - 1];
+            const ChunkArrays &arr = reinterpret_cast<const ChunkArrays *>(sm + OFF_ARR)[c % 3];
+            const float gam = arr.gamma[row], tail = arr.tail[row], bet = arr.beta[row], gC = arr.gamma[kC - 1];
             const P2 b2 = pk(bet, bet), bg = pk(-bet * gam, -bet * gam), t2 = pk(tail, tail), g2 = pk(gC, gC);
             if (ok) ok = bar_wait(bar_v, c & 1, spin);
             if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);  // P U has read U
@@ -549,22 +524,38 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
 }  // namespace
 
-cudaError_t delta_chunked_launch(const DeltaArgs &a, const void *t, cudaStream_t s)
+namespace {
+template <bool STATES>
+cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cudaStream_t s)
 {
     if (a.nseq * a.H == 0) return cudaSuccess;
     CUtensorMap mq, mk, mv;
-    if (!make_map(&mq, a.q, a.B, a.T, a.Hk) || !make_map(&mk, a.k, a.B, a.T, a.Hk) || !make_map(&mv, a.v, a.B, a.T, a.H))
+    if (!make_map(&mq, STATES ? a.k : a.q, a.B, a.T, a.Hk) || !make_map(&mk, a.k, a.B, a.T, a.Hk) ||
+        !make_map(&mv, a.v, a.B, a.T, a.H))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(delta_chunked_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    auto kern = delta_chunked_kernel<STATES>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(delta_chunked_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     const Params p{a.B, a.T, a.Hk, a.H, a.nseq, a.nslots, a.offsets, a.slots, static_cast<const __nv_bfloat16 *>(a.g),
                    static_cast<const __nv_bfloat16 *>(a.beta), static_cast<const unsigned char *>(t), delta_chunks(a),
-                   a.scale, a.s0, static_cast<__nv_bfloat16 *>(a.o), a.sT, a.status,
-                   g_chunked_inject_timeout ? 100u : 100000u, g_chunked_inject_timeout};
-    delta_chunked_kernel<<<static_cast<unsigned>(a.nseq * a.H), kThreads, kSmemBytes, s>>>(mq, mk, mv, p);
+                   a.scale, a.s0, static_cast<__nv_bfloat16 *>(a.o), a.sT, static_cast<unsigned char *>(states),
+                   static_cast<unsigned char *>(us), a.status, g_chunked_inject_timeout ? 100u : 100000u,
+                   g_chunked_inject_timeout};
+    kern<<<static_cast<unsigned>(a.nseq * a.H), kThreads, kSmemBytes, s>>>(mq, mk, mv, p);
     return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t delta_chunked_launch(const DeltaArgs &a, const void *t, cudaStream_t s)
+{
+    return launch<false>(a, t, nullptr, nullptr, s);
+}
+
+cudaError_t delta_states_launch(const DeltaArgs &a, const void *t, void *states, void *us, cudaStream_t s)
+{
+    return launch<true>(a, t, states, us, s);
 }
 
 }  // namespace wkv

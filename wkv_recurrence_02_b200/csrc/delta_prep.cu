@@ -135,23 +135,9 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     const int tid = threadIdx.x, lane = tid & 31;
     const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int64_t h = blockIdx.x % p.H, id = blockIdx.x / p.H, hk = h / (p.H / p.Hk);
-    // the sequence whose run of chunk numbers holds this one
     int64_t seq, first, len;
-    if (p.offsets) {
-        int64_t lo = 0, hi = p.nseq;  // last sequence whose run starts at or before id
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) / 2;
-            sequence_span(p.offsets, mid, p.T, &first, &len);
-            if (first_chunk(true, mid, first, p.T) <= id) lo = mid;
-            else hi = mid;
-        }
-        seq = lo;
-    } else {
-        seq = id / ((p.T + kC - 1) / kC);
-    }
-    sequence_span(p.offsets, seq, p.T, &first, &len);
-    const int64_t c = id - first_chunk(p.offsets != nullptr, seq, first, p.T);
-    if (c < 0 || c * kC >= len) return;  // a number that no chunk has
+    const int64_t c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
+    if (c < 0) return;  // a number that no chunk has
     const int64_t t0 = first + c * kC, ntok = p.B * p.T;
     const int tv = static_cast<int>(len - c * kC < kC ? len - c * kC : kC);
     const uint32_t bar = smem_u32(sm + OFF_BAR);

@@ -67,6 +67,8 @@ __device__ __forceinline__ uint64_t udesc_plain(uint32_t addr, uint32_t lbo, uin
 }
 // read along its rows (T W): K steps of 16 columns are 2048 bytes
 __device__ __forceinline__ uint64_t desc_t(uint32_t addr) { return udesc_plain(addr, 1024, 128); }
+// read across them (T^T dU): K steps of 16 rows are 256 bytes
+__device__ __forceinline__ uint64_t desc_tt(uint32_t addr) { return udesc_plain(addr, 128, 1024); }
 __host__ __device__ constexpr int t_stored_at(int c)  // byte offset of core column c in a stored term
 {
     return 256 * (8 * (c / 2) - (c / 2) * (c / 2 - 1)) + (c & 1) * (8 - 2 * (c / 2)) * 128;
@@ -78,6 +80,28 @@ static_assert(t_stored_at(7) + 256 == kTStored, "stored blocks of T");
 __host__ __device__ __forceinline__ int64_t first_chunk(bool packed, int64_t seq, int64_t first, int64_t T)
 {
     return packed ? first / kC + seq : seq * ((T + kC - 1) / kC);
+}
+
+// The chunk with number id: its place in its sequence (returned, -1 if no chunk has the number) and
+// the sequence.
+__device__ __forceinline__ int64_t chunk_of(const int32_t *offsets, int64_t nseq, int64_t T, int64_t id, int64_t *seq,
+                                            int64_t *first, int64_t *len)
+{
+    if (offsets) {
+        int64_t lo = 0, hi = nseq;  // last sequence whose run starts at or before id
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) / 2;
+            sequence_span(offsets, mid, T, first, len);
+            if (first_chunk(true, mid, *first, T) <= id) lo = mid;
+            else hi = mid;
+        }
+        *seq = lo;
+    } else {
+        *seq = id / ((T + kC - 1) / kC);
+    }
+    sequence_span(offsets, *seq, T, first, len);
+    const int64_t c = id - first_chunk(offsets != nullptr, *seq, *first, T);
+    return c >= 0 && c * kC < *len ? c : -1;
 }
 
 // fp32 pair -> bf16 pair hi and the bf16 pair of what hi leaves
@@ -160,6 +184,99 @@ __device__ __forceinline__ BlockSums block_sums(float g, int t)
         }
     }
     return {n, f, __shfl_sync(0xffffffffu, n, 15, 16), __shfl_sync(0xffffffffu, f, 15, 16)};
+}
+
+// Decays of one chunk, as a group of warps keeps them in shared memory.
+struct Decays {
+    float pn[kC], pf[kC];  // sums of log2 decays inside the block: integer and fraction part
+    float cf[kC];          // decay from after the token to its block's end
+    float pre[kC];         // decay from the block's start up to the token
+    float bs[8];           // integer, fraction parts of the blocks' sums
+};
+struct ChunkArrays {
+    float gamma[kC], tail[kC], beta[kC];
+};
+// Written by 64 threads (two whole warps), thread t with token t's g and beta (0 past the end);
+// named barrier ID among them.
+template <int ID> __device__ __forceinline__ void scan_decays(Decays &d, ChunkArrays &a, int t, float g, float beta)
+{
+    const int wb = t >> 4;
+    const BlockSums s = block_sums(g, t);
+    d.pn[t] = s.n;
+    d.pf[t] = s.f;
+    d.cf[t] = ex2_approx((s.bn - s.n) + (s.bf - s.f));
+    d.pre[t] = ex2_approx(s.n + s.f);
+    a.beta[t] = beta;
+    if ((t & 15) == 15) {
+        d.bs[wb] = s.n;
+        d.bs[4 + wb] = s.f;
+    }
+    group_sync<ID, 64>();
+    float gn = s.n, gf = s.f, tn = s.bn - s.n, tf = s.bf - s.f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        if (m < wb) gn += d.bs[m], gf += d.bs[4 + m];
+        if (m > wb) tn += d.bs[m], tf += d.bs[4 + m];
+    }
+    a.gamma[t] = ex2_approx(gn + gf);
+    a.tail[t] = ex2_approx(tn + tf);
+}
+__device__ __forceinline__ float widen(uint16_t bf16) { return __uint_as_float(static_cast<uint32_t>(bf16) << 16); }
+
+// Block row w of P from Q K^T in tensor memory (this warp's lanes), as bf16 pairs in the layout of
+// mma.sync accumulators; pl: what ph leaves, with LO.  Blocks right of the diagonal are zero.
+// `read` is called once the products have been read.
+template <bool LO, typename F>
+__device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_t qk, float scale, uint32_t (&ph)[4][4],
+                                       uint32_t (&pl)[4][4], F read)
+{
+    const int g = lane >> 2, t = lane & 3, r0 = 16 * w + g;
+    float x[4][2][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j <= w) tmem_ld_frag(qk + 16 * j, x[j]);
+    const float n0 = d.pn[r0], n1 = d.pn[r0 + 8], f0 = d.pf[r0], f1 = d.pf[r0 + 8];
+    const float p0 = scale * d.pre[r0], p1 = scale * d.pre[r0 + 8];
+    tmem_wait_ld();
+    read();
+    float mn = 0.f, mf = 0.f;  // decay of the whole blocks between block j and this one
+#pragma unroll
+    for (int j = 3; j >= 0; --j) {
+        if (j > w) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ph[j][i] = pl[j][i] = 0;
+            continue;
+        }
+        const float mid = ex2_approx(mn + mf);
+        if (j < w) mn += d.bs[j], mf += d.bs[4 + j];
+#pragma unroll
+        for (int nn = 0; nn < 2; ++nn) {
+            P2 gam[2];
+            if (j == w) {
+                const int col = 8 * nn + 2 * t;
+                const P2 cn = ld_p2(d.pn + 16 * j + col), ff = ld_p2(d.pf + 16 * j + col);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float e0 = ex2_approx(((r ? n1 : n0) - tc::lo(cn)) + ((r ? f1 : f0) - tc::lo(ff)));
+                    const float e1 = ex2_approx(((r ? n1 : n0) - tc::hi(cn)) + ((r ? f1 : f0) - tc::hi(ff)));
+                    gam[r] = pk(col <= g + 8 * r ? scale * e0 : 0.f, col + 1 <= g + 8 * r ? scale * e1 : 0.f);
+                }
+            } else {
+                const P2 cc = ld_p2(d.cf + 16 * j + 8 * nn + 2 * t);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float f = mid * (r ? p1 : p0);
+                    gam[r] = mul2(cc, pk(f, f));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const P2 y = mul2(gam[r], pk(x[j][nn][2 * r], x[j][nn][2 * r + 1]));
+                if (LO) split2(y, &ph[j][2 * nn + r], &pl[j][2 * nn + r]);
+                else ph[j][2 * nn + r] = pack2(y);
+            }
+        }
+    }
 }
 
 // A block of a swizzled 64 x 64 tile (rows 16 w, columns 16 j) from mma.sync accumulators' layout.

@@ -440,7 +440,9 @@ int delta_bwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int6
     if (!mul_ok(T / 8 + z->nseq + 2, H, &per) || !mul_ok(per, B > 0 ? B : 1, &all) || !mul_ok(all, 8192, &all))
         return fail(RWKV_ERR_SHAPE, "workspace size overflows%s");
     const wkv::DeltaArgs a = delta_shape(B, T, Hk, H, *z, packed, bf16);
-    *bytes = z->nseq > 0 && z->nh > 0 && N == 64 ? wkv::delta_walks_workspace_bytes(a) : 0;
+    *bytes = z->nseq == 0 || z->nh == 0 || N != 64 ? 0
+             : delta_chunked(T, *z, packed, bf16)  ? wkv::delta_backward_tc_workspace_bytes(a)
+                                                   : wkv::delta_walks_workspace_bytes(a);
     return RWKV_OK;
 }
 
@@ -492,7 +494,9 @@ int delta_bwd_entry(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, cons
     a.f = wkv::DeltaArgs{B, T, Hk, H, z.nseq, offsets, z.nseq, nullptr, q, k, v, g, beta, scale, s0, nullptr, nullptr, bf16, status};
     a.dout = dout, a.dsT = dsT, a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.ds0 = ds0;
     a.workspace = workspace;
-    const cudaError_t err = wkv::delta_backward_walks_launch(a, tl_stream);
+    const cudaError_t err = delta_chunked(T, z, offsets != nullptr, bf16)
+                                ? wkv::delta_backward_tc_launch(a, tl_stream)
+                                : wkv::delta_backward_walks_launch(a, tl_stream);
     return err == cudaSuccess ? RWKV_OK : cuda_fail(err, "delta backward launch");
 }
 

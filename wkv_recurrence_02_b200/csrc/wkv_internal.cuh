@@ -188,6 +188,8 @@ int64_t delta_chunks(const DeltaArgs &a);
 size_t delta_t_bytes(const DeltaArgs &a);
 cudaError_t delta_prep_launch(const DeltaArgs &a, void *t_out, cudaStream_t s);
 cudaError_t delta_chunked_launch(const DeltaArgs &a, const void *t, cudaStream_t s);
+// The state before every chunk and the updates U, bf16, as images of 8 KB tiles ([chunks][H]).
+cudaError_t delta_states_launch(const DeltaArgs &a, const void *t, void *states, void *us, cudaStream_t s);
 
 // Gated delta rule backward; gradients in the type of the inputs, state gradients fp32.
 struct DeltaBwdArgs {
@@ -201,6 +203,10 @@ struct DeltaBwdArgs {
     void *workspace;
 };
 size_t delta_walks_workspace_bytes(const DeltaArgs &a);
+size_t delta_backward_tc_workspace_bytes(const DeltaArgs &a);  // bf16
+cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s);
+// dq and dk of a key head: the fp32 shares [B,T,H,64] of its value heads, added in order.
+cudaError_t delta_sum_heads_launch(const DeltaBwdArgs &a, const float *dq_h, const float *dk_h, cudaStream_t s);
 cudaError_t delta_backward_walks_launch(const DeltaBwdArgs &a, cudaStream_t s);
 
 // First token and length of sequence i, clamped to the tokens there are, whatever the offsets say.
