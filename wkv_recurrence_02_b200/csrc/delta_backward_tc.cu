@@ -483,20 +483,26 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 }
 
 // ----------------------------------------------------------------------- gradients of a chunk
-// One block of eight warps per (chunk, value head), two per SM: warp (q, half) holds rows
-// 16 q .. 16 q + 15 and 32 of the 64 columns.  Eight tiles: what the walks left (U and S_prev side
-// by side: dW [U | S_prev]^T is one product of N = 128), Q, K, dO, and A1; A2 goes where dW was
-// (each thread overwrites what only it reads), diag(scale gamma) dO where dO was.
+// One block of eight warps per (chunk, value head), two per SM.  Warp (q, half) holds rows
+// 16 q .. 16 q + 15 and columns 32 half .. of every 64 x 64 result, thread (row, hl) columns 8 hl ..
+// 8 hl + 7 of both 16-wide blocks there: whether a block lies left of, on or right of the diagonal is
+// the same for the whole warp.  Two rounds of products:
+//   dO U^T, dW U^T, K K^T, Q K^T                     -> A1, A2, x
+//   diag(scale gamma) dO S_prev^T + A1 K, dW S_prev^T, (A2 + A2^T) K + A1^T Q, U dS^T -> the gradients
+// A1 and A2 enter the second round rounded to bf16.  For dg, where the terms of A1 and of A2 can
+// cancel (keys near one another), what the rounding left is added back as its row and column sums.
+// Nine tiles: Q, K, dO (then diag(scale gamma) dO in its place), U, S_prev, dW, dS, A1, A2.
 constexpr int kGThreads = 256;
 constexpr int GO_Q = 0, GO_K = kTile, GO_DO = 2 * kTile, GO_U = 3 * kTile, GO_S = 4 * kTile, GO_DW = 5 * kTile;
-constexpr int GO_DS = 6 * kTile, GO_A1 = 7 * kTile, GO_DEC = 8 * kTile;
+constexpr int GO_DS = 6 * kTile, GO_A1 = 7 * kTile, GO_A2 = 8 * kTile, GO_DEC = 9 * kTile;
 constexpr int GO_ARR = GO_DEC + static_cast<int>(sizeof(Decays));
 constexpr int GO_RED = GO_ARR + static_cast<int>(sizeof(ChunkArrays));  // [4 sums][2 halves][64], [8] warps' sums, [4]
-constexpr int GO_DIAG = GO_RED + 4 * 2 * 256 + 64;  // [64] diagonal of A1
+constexpr int GO_COL = GO_RED + 4 * 2 * 256 + 64;   // [4 block rows][64] column sums
+constexpr int GO_DIAG = GO_COL + 4 * 256;           // [64] diagonal of A1
 constexpr int GO_BAR = GO_DIAG + 256;
 constexpr int kGSmemBytes = GO_BAR + 32 + 1024;
-constexpr uint32_t GC_DOU = 0, GC_DWU = 64, GC_DWS = 128, GC_KK = 192;     // first products
-constexpr uint32_t GC_DQ = GC_DOU, GC_DK = GC_DWU, GC_UDS = GC_KK;         // second ones
+constexpr uint32_t GC_DOU = 0, GC_DWU = 64, GC_QK = 128, GC_KK = 192;           // first round
+constexpr uint32_t GC_DQ = 0, GC_DK = 64, GC_DWS = 128, GC_UDS = 192;           // second
 
 struct GradParams {
     int64_t B, T, Hk, H, nseq;
@@ -511,47 +517,79 @@ struct GradParams {
     uint32_t spin_limit;
 };
 
-// 16 of 32 columns of this thread's row: threads 0-15 columns c .. c + 15, threads 16-31 the next 16.
-__device__ __forceinline__ void tmem_ld_part(uint32_t taddr, float (&v)[16])
-{
+// A thread's 16 columns, as pairs: [4 b + i] of block b (b = 0, 1).
+struct Row {
+    P2 x[8];
+};
+struct Raw {
     uint32_t r[16];
-    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                   "=r"(r[15])
-                 : "r"(taddr));
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 16 bf16 of a swizzled tile's row
-__device__ __forceinline__ void ld_row16(const unsigned char *tile, int row, int col, float (&x)[16])
+};
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, Raw &v)  // no wait
 {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 y = *reinterpret_cast<const uint4 *>(tile + swz(row, 2 * col + 16 * i));
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    for (int b = 0; b < 2; ++b)
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
+                     : "=r"(v.r[8 * b]), "=r"(v.r[8 * b + 1]), "=r"(v.r[8 * b + 2]), "=r"(v.r[8 * b + 3]),
+                       "=r"(v.r[8 * b + 4]), "=r"(v.r[8 * b + 5]), "=r"(v.r[8 * b + 6]), "=r"(v.r[8 * b + 7])
+                     : "r"(taddr + 16 * b));
+}
+__device__ __forceinline__ Row row_of(Raw &v)  // after the wait
+{
+    Row y;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
-            x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
+    for (int i = 0; i < 16; ++i) after_wait(v.r[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y.x[i] = pk(__uint_as_float(v.r[2 * i]), __uint_as_float(v.r[2 * i + 1]));
+    return y;
+}
+__device__ __forceinline__ void unpack_row(const uint4 (&y)[2], Row &v)
+{
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        v.x[4 * b] = unpack2(y[b].x);
+        v.x[4 * b + 1] = unpack2(y[b].y);
+        v.x[4 * b + 2] = unpack2(y[b].z);
+        v.x[4 * b + 3] = unpack2(y[b].w);
     }
 }
-__device__ __forceinline__ void st_global16(__nv_bfloat16 *p, const float (&x)[16])
+__device__ __forceinline__ uint4 pack_block(const Row &v, int b)
 {
-    uint4 *dst = reinterpret_cast<uint4 *>(p);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                            pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+    return make_uint4(pack2(v.x[4 * b]), pack2(v.x[4 * b + 1]), pack2(v.x[4 * b + 2]), pack2(v.x[4 * b + 3]));
 }
-__device__ __forceinline__ void st_global16(float *p, const float (&x)[16])
+__device__ __forceinline__ float sum2(P2 x) { return lo(x) + hi(x); }
+__device__ __forceinline__ float dot(const Row &a, const Row &b)
+{
+    P2 s = mul2(a.x[0], b.x[0]), r = mul2(a.x[1], b.x[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        s = fma2(a.x[i], b.x[i], s);
+        r = fma2(a.x[i + 1], b.x[i + 1], r);
+    }
+    return sum2(add2(s, r));
+}
+// 8 columns (4 pairs) summed over the 16 rows of a half-warp: the total of column (lane >> 1) & 7
+__device__ __forceinline__ float column_sum(const P2 (&d)[4], int lane)
+{
+    const bool b8 = lane & 8, b4 = lane & 4, b2 = lane & 2;
+    P2 y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y[i] = add2(b8 ? d[2 + i] : d[i], shfl_xor2(b8 ? d[i] : d[2 + i], 8));
+    const P2 z = add2(b4 ? y[1] : y[0], shfl_xor2(b4 ? y[0] : y[1], 4));
+    float s = (b2 ? hi(z) : lo(z)) + __shfl_xor_sync(0xffffffffu, b2 ? lo(z) : hi(z), 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    return s;
+}
+__device__ __forceinline__ void st_blocks(__nv_bfloat16 *p, const Row &v)
+{
+    *reinterpret_cast<uint4 *>(p) = pack_block(v, 0);
+    *reinterpret_cast<uint4 *>(p + 16) = pack_block(v, 1);
+}
+__device__ __forceinline__ void st_blocks(float *p, const Row &v)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        *reinterpret_cast<float4 *>(p + 16 * (i >> 1) + 4 * (i & 1)) =
+            make_float4(lo(v.x[2 * i]), hi(v.x[2 * i]), lo(v.x[2 * i + 1]), hi(v.x[2 * i + 1]));
 }
 
 __global__ void __launch_bounds__(kGThreads, 2)
@@ -562,24 +600,26 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int64_t h = blockIdx.x % p.H, id = blockIdx.x / p.H, hk = h / (p.H / p.Hk);
+    const uint32_t heads = static_cast<uint32_t>(p.H), id = blockIdx.x / heads;
+    const int64_t h = blockIdx.x % heads, hk = static_cast<uint32_t>(h) / (heads / static_cast<uint32_t>(p.Hk));
     int64_t seq, first, len;
-    const int64_t c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
+    const int c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
     if (c < 0) return;  // a number that no chunk has
-    const int64_t t0 = first + c * kC, ntok = p.B * p.T;
-    const int tv = static_cast<int>(len - c * kC < kC ? len - c * kC : kC);
+    const int64_t t0 = first + static_cast<int64_t>(c) * kC, ntok = p.B * p.T;
+    const int tv = static_cast<int>(len - (t0 - first) < kC ? len - (t0 - first) : kC);
     const uint32_t bar0 = smem_u32(sm + GO_BAR), bar1 = bar0 + 8, bar2 = bar0 + 16;
     volatile uint32_t *tm = reinterpret_cast<volatile uint32_t *>(sm + GO_BAR + 24);
     Decays &dec = *reinterpret_cast<Decays *>(sm + GO_DEC);
     ChunkArrays &arr = *reinterpret_cast<ChunkArrays *>(sm + GO_ARR);
     float *red = reinterpret_cast<float *>(sm + GO_RED), *diag = reinterpret_cast<float *>(sm + GO_DIAG);
+    float *cols = reinterpret_cast<float *>(sm + GO_COL);
 
     if (warp == 0) {
         if (lane == 0) {
             for (int i = 0; i < 3; ++i) bar_init(bar0 + 8 * i, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = static_cast<int>(p.offsets ? t0 : c * kC);
-            const int64_t tile = (id * p.H + h) * kTile;
+            const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = static_cast<int>(p.offsets ? t0 : t0 - first);
+            const int64_t tile = (static_cast<int64_t>(id) * p.H + h) * kTile;
             if (tma_coord_ok(p.status, 0, 2, kN, row_t, p.T) && in_bounds(p.status, id, 1, p.nchunks)) {
                 bar_expect_tx(bar0, 7 * kTile);
                 tma_load_4d(smem_u32(sm + GO_Q), &map_q, 0, static_cast<int>(hk), row_t, row_b, bar0);
@@ -605,25 +645,20 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         }
         scan_decays<1>(dec, arr, t, g, b);
     }
-    // this thread's row and its 16 columns; v of that place comes straight from global memory
-    const int q = warp & 3, half = warp >> 2, row = 16 * q + (lane & 15), blk = 2 * half + (lane >> 4), col = 16 * blk;
+    // this thread's row and the first of its columns; v of that place comes straight from memory
+    const int q = warp & 3, half = warp >> 2, row = 16 * q + (lane & 15), col = 32 * half + 8 * (lane >> 4);
     const int64_t token = t0 + row, at = (token * p.H + h) * kN + col;
     const bool valid = row < tv && in_bounds(p.status, token, 1, ntok);
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    const uint32_t sw[2] = {swz(row, 2 * col), swz(row, 2 * col + 32)};  // its place in a tile
+    uint4 vv[2] = {};
     if (valid) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 y = reinterpret_cast<const uint4 *>(p.v + at)[i];
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
-                v[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-            }
-        }
+        vv[0] = *reinterpret_cast<const uint4 *>(p.v + at);
+        vv[1] = *reinterpret_cast<const uint4 *>(p.v + at + 16);
     }
+    auto tile_row = [&](int tile, Row &x) {
+        const uint4 y[2] = {*reinterpret_cast<const uint4 *>(sm + tile + sw[0]), *reinterpret_cast<const uint4 *>(sm + tile + sw[1])};
+        unpack_row(y, x);
+    };
     fence_before();
     __syncthreads();
     fence_after();
@@ -641,94 +676,129 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         const uint32_t aU = smem_u32(sm + GO_U), aS = smem_u32(sm + GO_S), aW = smem_u32(sm + GO_DW);
         const uint32_t aD = smem_u32(sm + GO_DS), a1 = smem_u32(sm + GO_A1);
         if (warp == 0) {
-            const uint64_t dO = desc_k(aO), dU = desc_k(aU), dW = desc_k(aW), dK = desc_k(aK);
+            const uint64_t dO = desc_k(aO), dU = desc_k(aU), dW = desc_k(aW), dK = desc_k(aK), dQ = desc_k(aQ);
             if (elect_one()) {
                 mma_tile<kStepK, kStepK, false>(tbase + GC_DOU, dO, dU, idesc(64, 0, 0));
-                mma_tile<kStepK, kStepK, false>(tbase + GC_DWU, dW, dU, idesc(128, 0, 0));  // dW U^T, dW S_prev^T
+                mma_tile<kStepK, kStepK, false>(tbase + GC_DWU, dW, dU, idesc(64, 0, 0));
+                mma_tile<kStepK, kStepK, false>(tbase + GC_QK, dQ, dK, idesc(64, 0, 0));
                 mma_tile<kStepK, kStepK, false>(tbase + GC_KK, dK, dK, idesc(64, 0, 0));
                 mma_commit(bar1);
             }
             __syncwarp();
         }
         const float beta = arr.beta[row], gam = arr.gamma[row], tail = arr.tail[row];
-        // ---- dV and the row's dW.V; <dS, S_prev>
-        float dots = 0.f, dwv = 0.f;
+        // ---- dV and the row's dW.V; <dS, S_prev>; decays of the blocks left of the diagonal
+        float dots, dwv;
         {
-            float x[16], y[16];
-            ld_row16(sm + GO_DW, row, col, x);
+            Row x, y;
+            tile_row(GO_DW, x);
+            unpack_row(vv, y);
+            dwv = dot(x, y);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                dwv = fmaf(x[i], v[i], dwv);
-                x[i] *= beta;
+            for (int i = 0; i < 8; ++i) x.x[i] = mul2(x.x[i], pk(beta, beta));
+            if (valid) st_blocks(p.dv + at, x);
+            tile_row(GO_S, x);
+            tile_row(GO_DS, y);
+            dots = dot(x, y);
+        }
+        Row gm;  // Gamma, zero right of the diagonal; 1 on it
+        const float n0 = dec.pn[row], f0 = dec.pf[row];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int blk = 2 * half + b;
+            if (blk < q) {
+                float mn = 0.f, mf = 0.f;
+#pragma unroll
+                for (int m = 1; m < 3; ++m)
+                    if (m > blk && m < q) mn += dec.bs[m], mf += dec.bs[4 + m];
+                const float rf = ex2_approx((n0 + mn) + (f0 + mf));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gm.x[4 * b + i] = mul2(ld_p2(dec.cf + col + 16 * b + 2 * i), pk(rf, rf));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int cc = col + 16 * b + 2 * i;
+                    const P2 cn = ld_p2(dec.pn + cc), cff = ld_p2(dec.pf + cc);
+                    gm.x[4 * b + i] = pk(cc <= row ? ex2_approx((n0 - lo(cn)) + (f0 - lo(cff))) : 0.f,
+                                         cc + 1 <= row ? ex2_approx((n0 - hi(cn)) + (f0 - hi(cff))) : 0.f);
+                }
             }
-            if (valid) st_global16(p.dv + at, x);
-            ld_row16(sm + GO_S, row, col, x);
-            ld_row16(sm + GO_DS, row, col, y);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dots = fmaf(x[i], y[i], dots);
         }
         ok = bar_wait(bar1, 0, p.spin_limit);
         fence_after();
-        // ---- A1, A2 and x = gamma K.(dW S_prev^T) + sum Gamma (k k) (dW.U)
-        float xt = 0.f, kr[16];
-        ld_row16(sm + GO_K, row, col, kr);
+        // ---- A1, A2, sum Gamma (k k) (dW.U), and what rounding A1 and A2 leaves
+        float xt = 0.f, rowd = 0.f;
         {
-            float s[16];
-            tmem_ld_part(tl + GC_DWS, s);
+            Raw ro, rw, rq, rk;
+            tmem_ld_blocks(tl + GC_DOU, ro);
+            tmem_ld_blocks(tl + GC_DWU, rw);
+            tmem_ld_blocks(tl + GC_QK, rq);
+            tmem_ld_blocks(tl + GC_KK, rk);
+            tmem_wait_ld();
+            const Row o = row_of(ro), wu = row_of(rw), qk = row_of(rq), kk = row_of(rk);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) xt = fmaf(kr[i], s[i], xt);
-            xt *= gam;
-        }
-        {
-            float o[16], wu[16], kk[16];
-            tmem_ld_part(tl + GC_DOU, o);
-            tmem_ld_part(tl + GC_DWU, wu);
-            tmem_ld_part(tl + GC_KK, kk);
-            const float n0 = dec.pn[row], f0 = dec.pf[row];
-            float mn = 0.f, mf = 0.f;
+            for (int b = 0; b < 2; ++b) {
+                const int blk = 2 * half + b;
+                uint32_t h1[4] = {}, h2[4] = {};
+                if (blk <= q) {
+                    P2 left[4], xs = pk(0.f, 0.f), rows = xs;
 #pragma unroll
-            for (int m = 1; m < 3; ++m)
-                if (m > blk && m < q) mn += dec.bs[m], mf += dec.bs[4 + m];
-            const float rf = ex2_approx((n0 + mn) + (f0 + mf));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float gm = 0.f;
-                if (blk < q) gm = rf * dec.cf[col + i];
-                else if (blk == q && i <= (lane & 15)) gm = ex2_approx((n0 - dec.pn[col + i]) + (f0 - dec.pf[col + i]));
-                o[i] *= p.scale * gm;
-                if (blk == q && i == (lane & 15)) {  // A1's diagonal is added to dQ and dK at the end
-                    diag[row] = o[i];
-                    o[i] = gm = 0.f;
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = 4 * b + i, cc = col + 16 * b + 2 * i;
+                        P2 a1 = mul2(mul2(gm.x[k], pk(p.scale, p.scale)), o.x[k]), g = gm.x[k];
+                        if (blk == q) {  // A1's diagonal is added to dQ and dK at the end
+                            if (cc == row) diag[row] = lo(a1);
+                            if (cc + 1 == row) diag[row] = hi(a1);
+                            a1 = pk(cc < row ? lo(a1) : 0.f, cc + 1 < row ? hi(a1) : 0.f);
+                            g = pk(cc < row ? lo(g) : 0.f, cc + 1 < row ? hi(g) : 0.f);
+                        }
+                        const P2 gw = mul2(g, wu.x[k]);
+                        xs = fma2(gw, kk.x[k], xs);
+                        const P2 a2 = mul2(gw, pk(-beta, -beta));
+                        h1[i] = pack2(a1);
+                        h2[i] = pack2(a2);
+                        // x, taken twice, has A2's row sum unrounded already: its remainder counts the
+                        // other way there
+                        const P2 m1 = pk(-1.f, -1.f);
+                        const P2 d1 = mul2(fma2(unpack2(h1[i]), m1, a1), qk.x[k]);
+                        const P2 d2 = mul2(fma2(unpack2(h2[i]), m1, a2), kk.x[k]);
+                        left[i] = add2(d1, d2);
+                        rows = add2(rows, fma2(d2, m1, d1));
+                    }
+                    xt += sum2(xs);
+                    rowd += sum2(rows);
+                    const float s = column_sum(left, lane);
+                    if ((lane & 1) == 0) cols[64 * q + col + 16 * b + ((lane >> 1) & 7)] = s;
                 }
-                const float gw = gm * wu[i];
-                xt = fmaf(gw, kk[i], xt);
-                wu[i] = -beta * gw;
+                *reinterpret_cast<uint4 *>(sm + GO_A1 + sw[b]) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+                *reinterpret_cast<uint4 *>(sm + GO_A2 + sw[b]) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
             }
-            st_row16_bf16(sm + GO_A1, row, 2 * col, o);
-            st_row16_bf16(sm + GO_DW, row, 2 * col, wu);
         }
         {
-            float x[16];
+            Row x;
             const float sg = p.scale * gam;
-            ld_row16(sm + GO_DO, row, col, x);
+            tile_row(GO_DO, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= sg;
-            st_row16_bf16(sm + GO_DO, row, 2 * col, x);
+            for (int i = 0; i < 8; ++i) x.x[i] = mul2(x.x[i], pk(sg, sg));
+            *reinterpret_cast<uint4 *>(sm + GO_DO + sw[0]) = pack_block(x, 0);
+            *reinterpret_cast<uint4 *>(sm + GO_DO + sw[1]) = pack_block(x, 1);
         }
         fence_async_smem();
         fence_before();
         ok = !__syncthreads_or(!ok);
         fence_after();
         if (warp == 0 && ok) {
-            const uint64_t dO = desc_k(aO), dS = desc_k(aS), dA1 = desc_k(a1), dA1t = desc_mn(a1), dA2 = desc_k(aW), dA2t = desc_mn(aW);
-            const uint64_t dKn = desc_mn(aK), dQn = desc_mn(aQ), dU = desc_k(aU), dD = desc_k(aD);
+            const uint32_t a2 = smem_u32(sm + GO_A2);
+            const uint64_t dO = desc_k(aO), dS = desc_k(aS), dA1 = desc_k(a1), dA1t = desc_mn(a1), dA2 = desc_k(a2), dA2t = desc_mn(a2);
+            const uint64_t dKn = desc_mn(aK), dQn = desc_mn(aQ), dU = desc_k(aU), dD = desc_k(aD), dW = desc_k(aW);
             if (elect_one()) {
                 mma_tile<kStepK, kStepK, false>(tbase + GC_DQ, dO, dS, idesc(64, 0, 0));
                 mma_tile<kStepK, kStepMn, true>(tbase + GC_DQ, dA1, dKn, idesc(64, 0, 1));
+                mma_tile<kStepK, kStepK, false>(tbase + GC_DWS, dW, dS, idesc(64, 0, 0));
+                mma_tile<kStepK, kStepK, false>(tbase + GC_UDS, dU, dD, idesc(64, 0, 0));
                 mma_tile<kStepK, kStepMn, false>(tbase + GC_DK, dA2, dKn, idesc(64, 0, 1));
                 mma_tile<kStepMn, kStepMn, true>(tbase + GC_DK, dA2t, dKn, idesc(64, 1, 1));
                 mma_tile<kStepMn, kStepMn, true>(tbase + GC_DK, dA1t, dQn, idesc(64, 1, 1));
-                mma_tile<kStepK, kStepK, false>(tbase + GC_UDS, dU, dD, idesc(64, 0, 0));
                 mma_commit(bar2);
             }
             __syncwarp();
@@ -738,32 +808,41 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         fence_after();
         {
             const float a = diag[row], bg = -beta * gam;
-            float x[16], y[16], z[16], qr[16];
-            tmem_ld_part(tl + GC_DQ, x);
-            ld_row16(sm + GO_Q, row, col, qr);
+            const P2 a2 = pk(a, a);
+            Row qr, kr;
+            Raw rx, ry, rz;
+            tmem_ld_blocks(tl + GC_DQ, rx);
+            tile_row(GO_Q, qr);
+            tile_row(GO_K, kr);
+            tmem_wait_ld();
+            Row x = row_of(rx);
+            e = dot(x, qr) + rowd;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                e = fmaf(x[i], qr[i], e);
-                x[i] = fmaf(a, kr[i], x[i]);
-            }
+            for (int i = 0; i < 8; ++i) x.x[i] = fma2(a2, kr.x[i], x.x[i]);
             if (valid) {
-                if (p.dq_h) st_global16(p.dq_h + at, x);
-                else st_global16(p.dq + at, x);
+                if (p.dq_h) st_blocks(p.dq_h + at, x);
+                else st_blocks(p.dq + at, x);
             }
-            tmem_ld_part(tl + GC_DK, x);
-            tmem_ld_part(tl + GC_DWS, y);
-            tmem_ld_part(tl + GC_UDS, z);
+            tmem_ld_blocks(tl + GC_DK, rx);
+            tmem_ld_blocks(tl + GC_DWS, ry);
+            tmem_ld_blocks(tl + GC_UDS, rz);
+            tmem_wait_ld();
+            x = row_of(rx);
+            const Row y = row_of(ry);
+            Row z = row_of(rz);
+            xt = fmaf(gam, dot(kr, y), xt);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[i] = fmaf(bg, y[i], x[i]);
-                e = fmaf(-kr[i], x[i], e);
-                z[i] *= tail;
-                r2 = fmaf(kr[i], z[i], r2);
-                x[i] += fmaf(a, qr[i], z[i]);
+            for (int i = 0; i < 8; ++i) {
+                x.x[i] = fma2(pk(bg, bg), y.x[i], x.x[i]);
+                z.x[i] = mul2(z.x[i], pk(tail, tail));
             }
+            e -= dot(kr, x);
+            r2 = dot(kr, z);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x.x[i] = add2(x.x[i], fma2(a2, qr.x[i], z.x[i]));
             if (valid) {
-                if (p.dk_h) st_global16(p.dk_h + at, x);
-                else st_global16(p.dk + at, x);
+                if (p.dk_h) st_blocks(p.dk_h + at, x);
+                else st_blocks(p.dk + at, x);
             }
         }
         // ---- sums over a row's four threads, and over the chunk
@@ -785,6 +864,7 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             const int t = tid;
             const float x = red[128 + t] + red[192 + t], own = red[384 + t] + red[448 + t];
             float s = red[256 + t] + red[320 + t] - 2.f * arr.beta[t] * x, before = own;
+            for (int i = t >> 4; i < 4; ++i) s -= cols[64 * i + t];  // rows from the column's own block on
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {  // from the token to its warp's last; from the first to the token
                 const float y = __shfl_down_sync(0xffffffffu, s, d), z = __shfl_up_sync(0xffffffffu, before, d);

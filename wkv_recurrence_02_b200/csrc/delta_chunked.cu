@@ -346,7 +346,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
             if (ok) ok = bar_wait(bar_a, c & 1, spin);
             fence_after();
-            uint32_t ph[4][4], pl[4][4];
+            uint32_t ph[4][4], pl[4][4];  // pl: unused
             form_p<false>(dec, w, lane, co + 64 * (c & 1), p.scale, ph, pl, [&] {
                 fence_before();
                 bar_arrive(bar_sr);

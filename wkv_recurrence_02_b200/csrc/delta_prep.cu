@@ -134,17 +134,18 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31;
     const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int64_t h = blockIdx.x % p.H, id = blockIdx.x / p.H, hk = h / (p.H / p.Hk);
+    const uint32_t heads = static_cast<uint32_t>(p.H), id = blockIdx.x / heads;
+    const int64_t h = blockIdx.x % heads, hk = static_cast<uint32_t>(h) / (heads / static_cast<uint32_t>(p.Hk));
     int64_t seq, first, len;
-    const int64_t c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
+    const int c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
     if (c < 0) return;  // a number that no chunk has
-    const int64_t t0 = first + c * kC, ntok = p.B * p.T;
-    const int tv = static_cast<int>(len - c * kC < kC ? len - c * kC : kC);
+    const int64_t t0 = first + static_cast<int64_t>(c) * kC, ntok = p.B * p.T;
+    const int tv = static_cast<int>(len - (t0 - first) < kC ? len - (t0 - first) : kC);
     const uint32_t bar = smem_u32(sm + OFF_BAR);
     if (tid == 0) {
         bar_init(bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = static_cast<int>(p.offsets ? t0 : c * kC);
+        const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = static_cast<int>(p.offsets ? t0 : t0 - first);
         if (tma_coord_ok(p.status, 0, 2, kN, row_t, p.T)) {
             bar_expect_tx(bar, kTile);
             tma_load_4d(smem_u32(sm), &map_k, 0, static_cast<int>(hk), row_t, row_b, bar);
@@ -291,7 +292,7 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
         return;
     }
     // ---- T
-    unsigned char *const tout = p.t_out + (id * p.H + h) * kTBytes;
+    unsigned char *const tout = p.t_out + (static_cast<int64_t>(id) * p.H + h) * kTBytes;
     if (!in_bounds(p.status, id, 1, p.nchunks)) return;
     auto L = [&](int k, int j) { return ld_block(sm + OFF_L + 1024 * (k * (k - 1) / 2 + j), lane); };
     auto D = [&](int j) { return ld_block(sm + OFF_X + 1024 * j, lane); };

@@ -83,25 +83,29 @@ __host__ __device__ __forceinline__ int64_t first_chunk(bool packed, int64_t seq
 }
 
 // The chunk with number id: its place in its sequence (returned, -1 if no chunk has the number) and
-// the sequence.
-__device__ __forceinline__ int64_t chunk_of(const int32_t *offsets, int64_t nseq, int64_t T, int64_t id, int64_t *seq,
-                                            int64_t *first, int64_t *len)
+// the sequence.  32-bit arithmetic: there are fewer than 2^31 tokens, sequences and chunks.
+__device__ __forceinline__ int chunk_of(const int32_t *offsets, int64_t nseq, int64_t T, uint32_t id, int64_t *seq,
+                                        int64_t *first, int64_t *len)
 {
+    const uint32_t tokens = static_cast<uint32_t>(T);
     if (offsets) {
-        int64_t lo = 0, hi = nseq;  // last sequence whose run starts at or before id
+        uint32_t lo = 0, hi = static_cast<uint32_t>(nseq);  // last sequence whose run starts at or before id
         while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) / 2;
-            sequence_span(offsets, mid, T, first, len);
-            if (first_chunk(true, mid, *first, T) <= id) lo = mid;
+            const uint32_t mid = (lo + hi) / 2;
+            const int at = min(max(offsets[mid], 0), static_cast<int>(tokens));
+            if (static_cast<uint32_t>(at) / kC + mid <= id) lo = mid;
             else hi = mid;
         }
         *seq = lo;
-    } else {
-        *seq = id / ((T + kC - 1) / kC);
+        sequence_span(offsets, lo, T, first, len);
+        const int c = static_cast<int>(id - (static_cast<uint32_t>(*first) / kC + lo));
+        return c >= 0 && static_cast<int64_t>(c) * kC < *len ? c : -1;
     }
-    sequence_span(offsets, *seq, T, first, len);
-    const int64_t c = id - first_chunk(offsets != nullptr, *seq, *first, T);
-    return c >= 0 && c * kC < *len ? c : -1;
+    const uint32_t per = (tokens + kC - 1) / kC;
+    *seq = id / per;
+    *first = *seq * T;
+    *len = T;
+    return static_cast<int>(id % per);
 }
 
 // fp32 pair -> bf16 pair hi and the bf16 pair of what hi leaves
@@ -110,6 +114,11 @@ __device__ __forceinline__ void split2(P2 x, uint32_t *hi, uint32_t *lo)
     *hi = pack2(x);
     *lo = pack2(fma2(unpack2(*hi), pk(-1.f, -1.f), x));
 }
+
+// A value loaded from tensor memory may be read only after the wait: this keeps the compiler from
+// moving even a copy of it before.
+__device__ __forceinline__ void after_wait(float &x) { asm volatile("" : "+f"(x)); }
+__device__ __forceinline__ void after_wait(uint32_t &x) { asm volatile("" : "+r"(x)); }
 
 // 16 TMEM lanes x 16 columns in the layout of mma.sync accumulators: v[n] holds columns 8 n + 2 t,
 // 8 n + 2 t + 1 of row g, then of row g + 8 (g = lane / 4, t = lane % 4).  No wait.
@@ -140,6 +149,11 @@ __device__ __forceinline__ void tmem_ld_sum16(uint32_t taddr, P2 (&x)[8])
     WKV_LD16(b, taddr + 64);
 #undef WKV_LD16
     tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        after_wait(a[i]);
+        after_wait(b[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         x[i] = add2(pk(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])),
@@ -231,14 +245,8 @@ __device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_
                                        uint32_t (&pl)[4][4], F read)
 {
     const int g = lane >> 2, t = lane & 3, r0 = 16 * w + g;
-    float x[4][2][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (j <= w) tmem_ld_frag(qk + 16 * j, x[j]);
     const float n0 = d.pn[r0], n1 = d.pn[r0 + 8], f0 = d.pf[r0], f1 = d.pf[r0 + 8];
     const float p0 = scale * d.pre[r0], p1 = scale * d.pre[r0 + 8];
-    tmem_wait_ld();
-    read();
     float mn = 0.f, mf = 0.f;  // decay of the whole blocks between block j and this one
 #pragma unroll
     for (int j = 3; j >= 0; --j) {
@@ -247,6 +255,12 @@ __device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_
             for (int i = 0; i < 4; ++i) ph[j][i] = pl[j][i] = 0;
             continue;
         }
+        float x[2][4];
+        tmem_ld_frag(qk + 16 * j, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) after_wait(x[i >> 2][i & 3]);
+        if (j == 0) read();
         const float mid = ex2_approx(mn + mf);
         if (j < w) mn += d.bs[j], mf += d.bs[4 + j];
 #pragma unroll
@@ -271,7 +285,7 @@ __device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const P2 y = mul2(gam[r], pk(x[j][nn][2 * r], x[j][nn][2 * r + 1]));
+                const P2 y = mul2(gam[r], pk(x[nn][2 * r], x[nn][2 * r + 1]));
                 if (LO) split2(y, &ph[j][2 * nn + r], &pl[j][2 * nn + r]);
                 else ph[j][2 * nn + r] = pack2(y);
             }
