@@ -35,8 +35,7 @@ using namespace dtc;
 //   chain group (warps 4-7)  dS -> K dS -> dU -> T^T dU = dW -> K^T diag(-beta gamma) dW -> dS
 //   side group (warps 0-3)   what the chain adds but does not wait for: Q K^T, P, P^T dO, and
 //                            Q^T diag(scale gamma) dO, where the chain's last product accumulates
-//   issuer (warp 8), loader (warp 9)
-constexpr int kThreads = 320;
+constexpr int kThreads = 256;
 // 13 tiles: K, Q and dO of two chunks, T (hi, lo), a pair for P hi/lo and then diag(scale gamma) dO
 // hi/lo, and the chain's A, B, C: dS hi/lo (A, B), dU hi/lo (B, C), diag(-beta gamma) dW hi/lo (A, B)
 // and dW (C)
@@ -84,30 +83,28 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
     const uint32_t bar_y = smem_u32(&bars[10]);    // Q^T diag(scale gamma) dO done
     const uint32_t bar_rr = smem_u32(&bars[11]);   // P^T dO read: its columns may take Q K^T
     const uint32_t bar_yr = smem_u32(&bars[12]);   // the new dS read: its columns may be written
-    const uint32_t bar_tf = smem_u32(&bars[13]);   // T has been read
-    const uint32_t bar_kf0 = smem_u32(&bars[14]);  // K, Q, dO have been read: + 8 * (n % 2)
-    const uint32_t bar_r = smem_u32(&bars[16]);    // dS, dU, dW written (three phases a chunk)
     const uint32_t bar_as = smem_u32(&bars[17]);   // the copies of dS, of dW have read them
     const uint32_t bar_cs = smem_u32(&bars[18]);
-    // decays written, tail rows zeroed: + 8 * (n % 3), since the side group may pass two more
-    // chunks here before the chain waits for this one
+    // decays written (for n = 0 also the tail rows zeroed): + 8 * (n % 3), since the side group may
+    // pass two more chunks here before the chain waits for this one
     const uint32_t bar_s0 = smem_u32(&bars[19]);
     const uint32_t bar_drain = smem_u32(&bars[22]);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, see elect_one
     const int64_t blk = blockIdx.x, seq = blk / p.H, h = blk % p.H, hk = h / (p.H / p.Hk);
-    int64_t first, len;
-    sequence_span(p.offsets, seq, p.T, &first, &len);
-    const int nchunks = static_cast<int>((len + kC - 1) / kC);
+    int64_t first_, len_;
+    sequence_span(p.offsets, seq, p.T, &first_, &len_);
+    const int first = static_cast<int>(first_), len = static_cast<int>(len_);  // fewer than 2^31 tokens in all
+    const int nchunks = (len + kC - 1) / kC;
     const int64_t chunk0 = first_chunk(p.offsets != nullptr, seq, first, p.T);
-    const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = p.offsets ? static_cast<int>(first) : 0;
+    const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = p.offsets ? first : 0;
     const uint32_t spin = p.spin_limit;
     const int64_t ntok = p.B * p.T;
 
     if (tid == 0) {
         for (int i = 0; i < 23; ++i)
-            bar_init(smem_u32(&bars[i]), i == 11 || i == 12 || i == 16 ? 128 : i == 22 ? 2 : i >= 19 ? 65 : 1);
+            bar_init(smem_u32(&bars[i]), i == 11 || i == 12 ? 128 : i == 22 ? 2 : i >= 19 ? 64 : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         misc[1] = 0;
     }
@@ -117,9 +114,6 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    for (int i = tid; i < 2 * kTile / 16; i += kThreads)  // T: the blocks above the diagonal, once
-        *reinterpret_cast<uint4 *>(sm + OFF_T + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-    fence_async_smem();
     fence_before();
     __syncthreads();
     fence_after();
@@ -136,100 +130,23 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         load_tile(&map_q, OFF_Q + kTile * (n & 1), hk, n, bar_q0 + 8 * (n & 1));
         load_tile(&map_do, OFF_DO + kTile * (n & 1), h, n, bar_g0 + 8 * (n & 1));
     };
-    auto load_t = [&](int n) {  // one warp, a copy for each of 8 core columns of each term
+    auto load_t = [&](int n) {  // one thread
         const int64_t id = chunk0 + nchunks - 1 - n;
         if (!in_bounds(p.status, id, 1, p.nchunks)) return;
-        if (lane == 0) bar_expect_tx(bar_t, kTBytes);
-        __syncwarp();
-        if (lane < 16) {
-            const int col = lane & 7, term = lane >> 3;
-            bulk_load(smem_u32(sm + OFF_T + kTile * term + 1024 * col + 256 * (col >> 1)),
-                      p.t + (id * p.H + h) * kTBytes + term * kTStored + t_stored_at(col), (8 - 2 * (col >> 1)) * 128,
-                      bar_t);
-        }
+        bar_expect_tx(bar_t, kTBytes);
+        bulk_load(smem_u32(sm + OFF_T), p.t + (id * p.H + h) * kTBytes, kTBytes, bar_t);
     };
-
-    int ok = 1;
-    if (warp == 9) {
-        // ---------------------------------------------------------------------- loader
-        // No wait by parity can be two phases late: dW of n + 1 needs the T loaded after the wait
-        // for dW of n; the new dS of n + 2 the K loaded after the wait for that of n (whose barriers
-        // alternate).
+    if (warp == 7) {
         for (int n = 0; n < 2 && n < nchunks; ++n) {
-            if (elect_one()) load_tiles(n);
+            if (elect_one()) {
+                load_tiles(n);
+                if (n == 0) load_t(0);
+            }
             __syncwarp();
         }
-        if (nchunks > 0) load_t(0);
-        for (int n = 0; n + 1 < nchunks && ok; ++n) {
-            ok = __all_sync(0xffffffffu, bar_wait(bar_tf, n & 1, spin));
-            if (!ok) break;
-            load_t(n + 1);
-            if (n + 2 >= nchunks) break;
-            ok = __all_sync(0xffffffffu, bar_wait(bar_kf0 + 8 * (n & 1), (n >> 1) & 1, spin));
-            if (ok && elect_one()) load_tiles(n + 2);
-            __syncwarp();
-        }
-    } else if (warp == 8) {
-        // ---------------------------------------------------------------------- issuer
-        const uint32_t tA = smem_u32(sm + OFF_A), tB = smem_u32(sm + OFF_B), tC = smem_u32(sm + OFF_CC);
-        const uint64_t dA = desc_mn(tA), dB = desc_mn(tB);
-        const uint64_t dTh = desc_tt(smem_u32(sm + OFF_T)), dTl = desc_tt(smem_u32(sm + OFF_T + kTile));
-        uint32_t rph = 0;
-        auto wait = [&](uint32_t bar, uint32_t phase) {
-            if (ok) ok = __all_sync(0xffffffffu, bar_wait_spin(bar, phase, spin * 64u));
-            fence_after();
-        };
-        for (int n = 0; n < nchunks && ok; ++n) {
-            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (n & 1));
-            const uint64_t dK = desc_k(aK), dKt = desc_mn(aK);
-            const int64_t id = chunk0 + nchunks - 1 - n, tile = (id * p.H + h) * kTile;
-            wait(bar_s0 + 8 * (n % 3), (n / 3) & 1);
-            wait(bar_r, rph);  // dS
-            rph ^= 1;
-            if (ok && lane == 0 && in_bounds(p.status, id, 1, p.nchunks)) {
-                bulk_store(p.ds + tile, tA, kTile);
-                bulk_commit();
-            }
-            if (ok && elect_one()) {  // K dS
-                mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, idesc(128, 0, 1));
-                mma_commit(bar_x);
-            }
-            __syncwarp();
-            if (lane == 0) {
-                bulk_wait_read<0>();
-                bar_arrive(bar_as);
-            }
-            wait(bar_t, n & 1);
-            wait(bar_r, rph);  // dU
-            rph ^= 1;
-            if (ok && elect_one()) {  // dW = T^T dU
-                mma_tile<kStepTMn, kStepMn, false>(tbase + COL_X, dTh, dB, idesc(128, 1, 1));
-                mma_tile<kStepTMn, kStepMn, true>(tbase + COL_X, dTl, dB, idesc(64, 1, 1));
-                mma_commit(bar_x);
-                mma_commit(bar_tf);
-            }
-            __syncwarp();
-            wait(bar_y, n & 1);
-            wait(bar_r, rph);  // dW
-            rph ^= 1;
-            if (ok && lane == 0 && in_bounds(p.status, id, 1, p.nchunks)) {
-                bulk_store(p.dw + tile, tC, kTile);
-                bulk_commit();
-            }
-            if (ok && elect_one()) {  // + K^T diag(-beta gamma) dW
-                mma_tile<kStepMn, kStepMn, true>(tbase + COL_Y, dKt, dA, idesc(64, 1, 1));
-                mma_tile<kStepMn, kStepMn, true>(tbase + COL_Y, dKt, dB, idesc(64, 1, 1));
-                mma_commit(bar_x);
-                mma_commit(bar_kf0 + 8 * (n & 1));  // Q and dO: read before bar_y
-            }
-            __syncwarp();
-            if (lane == 0) {
-                bulk_wait_read<0>();
-                bar_arrive(bar_cs);
-            }
-        }
-        if (lane == 0) bulk_wait_all();
-    } else if (warp < 4) {
+    }
+    int ok = 1, abort = 0;
+    if (warp < 4) {
         // ------------------------------------------------------------------ side group
         const int w = warp;
         Decays &dec = *reinterpret_cast<Decays *>(sm + OFF_DEC);
@@ -237,10 +154,10 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         const int st = tid - 64;
         uint16_t g_next = 0, b_next = 0;
         auto fetch = [&](int n) {  // g and beta of a token, a chunk ahead
-            const int64_t t = static_cast<int64_t>(nchunks - 1 - n) * kC + st;
+            const int t = (nchunks - 1 - n) * kC + st;
             g_next = b_next = 0;
             if (t >= len || !in_bounds(p.status, first + t, 1, ntok)) return;
-            const int64_t at = (first + t) * p.H + h;
+            const int64_t at = static_cast<int64_t>(first + t) * p.H + h;
             g_next = reinterpret_cast<const uint16_t *>(p.g)[at];
             b_next = reinterpret_cast<const uint16_t *>(p.beta)[at];
         };
@@ -257,7 +174,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                                bar_wait(bar_g0 + 8 * (n & 1), ph, spin) &&
                                (n == 0 || bar_wait(bar_rr, (n - 1) & 1, spin));
             if (!__all_sync(0xffffffffu, there)) return 0;
-            const int tv = static_cast<int>(len - static_cast<int64_t>(nchunks - 1 - n) * kC);
+            const int tv = len - (nchunks - 1 - n) * kC;
             if (tv < kC) {
                 zero_rows(kt, tv, lane, 32);
                 zero_rows(qt, tv, lane, 32);
@@ -270,7 +187,6 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             if (elect_one()) {
                 mma_tile<kStepK, kStepK, false>(tbase + COL_R, dq, dk, idesc(64, 0, 0));
                 mma_commit(bar_a);
-                bar_arrive(bar_s0 + 8 * (n % 3));
             }
             __syncwarp();
             return 1;
@@ -278,13 +194,12 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         const uint32_t qk = tbase + (static_cast<uint32_t>(32 * w) << 16) + COL_R;
         const int row = 16 * w + (lane & 15), col = 32 * (lane >> 4);
         unsigned char *ph_t = sm + OFF_PG, *pl_t = sm + OFF_PG + kTile;
-        int abort = 0;
         if (nchunks > 0) {
+            if (w == 0) ok = products(0);
+            group_sync<1, 128>();
             if (w >= 2) {
                 fetch(0);
                 scan(0);
-            } else if (w == 0) {
-                ok = products(0);
             }
         }
         for (int n = 0; n < nchunks && !abort; ++n) {
@@ -292,7 +207,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             if (ok) ok = bar_wait(bar_a, n & 1, spin);
             fence_after();
             uint32_t ph[4][4], pl[4][4];
-            form_p<true>(dec, w, lane, qk, p.scale, ph, pl, [] {});
+            form_p<true>(dec, w, lane, qk, p.scale, ph, pl);
             fence_before();
             if (named_sync_or(1, 128, !ok || misc[1])) {
                 abort = 1;
@@ -374,37 +289,63 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i] = pk(0.f, 0.f);
         }
-        uint32_t at[4];  // this thread's 32 columns of a tile
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = swz(row, 2 * col + 16 * i);
+        const uint32_t at0 = swz(row, 2 * col);  // this thread's 32 columns of a tile: i-th 16 bytes
+        auto at = [&](int i) { return at0 ^ static_cast<uint32_t>(16 * i); };
         auto store_split = [&](const P2 *x, int half, unsigned char *th, unsigned char *tlo) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t a[4], b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split2(x[4 * i + e], &a[e], &b[e]);
-                *reinterpret_cast<uint4 *>(th + at[2 * half + i]) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4 *>(tlo + at[2 * half + i]) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4 *>(th + at(2 * half + i)) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4 *>(tlo + at(2 * half + i)) = make_uint4(b[0], b[1], b[2], b[3]);
             }
         };
-        auto ready = [&]() {
+        const uint64_t dA = desc_mn(smem_u32(tA)), dB = desc_mn(smem_u32(tB));
+        const uint64_t dTh = desc_tt(smem_u32(sm + OFF_T)), dTl = desc_tt(smem_u32(sm + OFF_T + kTile));
+        auto meet = [&]() {  // what was written is ready for the products issued next
             fence_async_smem();
             fence_before();
-            bar_arrive(bar_r);
+            group_sync<2, 128>();
+            fence_after();
         };
         uint32_t xph = 0;  // phase of bar_x
         for (int n = 0; n < nchunks; ++n) {
-            if (!__all_sync(0xffffffffu, ok)) break;  // a wait ran out
-            // ---- dS hi, lo
+            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (n & 1));
+            const int64_t id = chunk0 + nchunks - 1 - n, tile = (id * p.H + h) * kTile;
+            // ---- dS hi, lo; K dS.  Whether to stop is voted on here
             store_split(S, 0, tA, tB);
             store_split(S + 8, 1, tA, tB);
-            ready();
+            if (ok) ok = bar_wait(bar_s0 + 8 * (n % 3), (n / 3) & 1, spin);
+            if (ok) ok = bar_wait(bar_k0 + 8 * (n & 1), (n >> 1) & 1, spin);
+            fence_async_smem();
+            fence_before();
+            if (named_sync_or(2, 128, !ok || misc[1])) {
+                abort = 1;
+                break;
+            }
+            fence_after();
+            if (warp == 4) {
+                const uint64_t dK = desc_k(aK);
+                if (elect_one()) {
+                    mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, idesc(128, 0, 1));
+                    mma_commit(bar_x);
+                }
+            } else if (warp == 5 && lane == 0) {
+                if (in_bounds(p.status, id, 1, p.nchunks)) bulk_store(p.ds + tile, smem_u32(tA), kTile);
+                bulk_commit();
+                bulk_wait_read<0>();
+                bar_arrive(bar_as);
+            } else if (warp == 7 && n > 0 && n + 1 < nchunks) {  // dS is there: the chunk before is done with its tiles
+                if (elect_one()) load_tiles(n + 1);
+            }
+            __syncwarp();
             // ---- dU = P^T dO + diag(tail) K dS
-            ok = bar_wait(bar_s0 + 8 * (n % 3), (n / 3) & 1, spin);
             const ChunkArrays &arr = reinterpret_cast<const ChunkArrays *>(sm + OFF_ARR)[n % 3];
             const float bg = -arr.beta[row] * arr.gamma[row], tail = arr.tail[row], gC = arr.gamma[kC - 1];
             if (ok) ok = bar_wait(bar_d0, n & 1, spin);
             if (ok && n > 0) ok = bar_wait(bar_cs, (n - 1) & 1, spin);
+            if (ok) ok = bar_wait(bar_t, n & 1, spin);
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
@@ -418,11 +359,19 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 for (int i = 0; i < 8; ++i) x[i] = fma2(pk(tail, tail), x[i], pk(d0[2 * i], d0[2 * i + 1]));
                 store_split(x, half, tB, tC);
             }
-            fence_before();
+            meet();
             bar_arrive(bar_rr);
-            ready();
+            if (warp == 4) {  // ---- dW = T^T dU
+                if (elect_one()) {
+                    mma_tile<kStepTMn, kStepMn, false>(tbase + COL_X, dTh, dB, idesc(128, 1, 1));
+                    mma_tile<kStepTMn, kStepMn, true>(tbase + COL_X, dTl, dB, idesc(64, 1, 1));
+                    mma_commit(bar_x);
+                }
+                __syncwarp();
+            }
             // ---- dW, and diag(-beta gamma) dW hi, lo
             if (ok) ok = bar_wait(bar_as, n & 1, spin);
+            if (ok) ok = bar_wait(bar_y, n & 1, spin);
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
@@ -432,13 +381,29 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 tmem_ld_sum16(tl + COL_X + 16 * half, x);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4 *>(tC + at[2 * half + i]) =
+                    *reinterpret_cast<uint4 *>(tC + at(2 * half + i)) =
                         make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], pk(bg, bg));
                 store_split(x, half, tA, tB);
             }
-            ready();
+            meet();
+            if (warp == 4) {  // ---- + K^T diag(-beta gamma) dW
+                const uint64_t dKt = desc_mn(aK);
+                if (elect_one()) {
+                    mma_tile<kStepMn, kStepMn, true>(tbase + COL_Y, dKt, dA, idesc(64, 1, 1));
+                    mma_tile<kStepMn, kStepMn, true>(tbase + COL_Y, dKt, dB, idesc(64, 1, 1));
+                    mma_commit(bar_x);
+                }
+            } else if (warp == 5 && lane == 0) {
+                if (in_bounds(p.status, id, 1, p.nchunks)) bulk_store(p.dw + tile, smem_u32(tC), kTile);
+                bulk_commit();
+                bulk_wait_read<0>();
+                bar_arrive(bar_cs);
+            } else if (warp == 7 && n + 1 < nchunks) {
+                if (elect_one()) load_t(n + 1);  // dW is there: T has been read
+            }
+            __syncwarp();
             // ---- dS
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
@@ -454,6 +419,8 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             fence_before();
             bar_arrive(bar_yr);
         }
+        if (warp == 5 && lane == 0) bulk_wait_all();
+        if (abort) ok = 0;
         if (ok && p.ds0 && in_bounds(p.status, sat, 32, nstate)) {
             float4 *dst = reinterpret_cast<float4 *>(p.ds0 + sat);
 #pragma unroll
@@ -464,11 +431,11 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 
     // ---- drain after an abort, then release tensor memory
     fence_before();
-    const int abort = __syncthreads_or(misc[1] != 0);
+    abort = __syncthreads_or(abort || misc[1] != 0);
     fence_after();
     if (abort) {
         record_status(p.status, kStatusTimeout);
-        if ((warp == 0 || warp == 8) && elect_one()) mma_commit(bar_drain);  // the two issuers
+        if ((warp == 0 || warp == 4) && elect_one()) mma_commit(bar_drain);  // the two issuers
         if (tid == 0) {
             bar_wait(bar_drain, 0, p.spin_limit);
             for (int i = 0; i < 7; ++i)  // copies in flight: a barrier that nothing will complete runs out

@@ -7,11 +7,9 @@
 // together do not stay in the instruction caches, and each ran at half its speed.)  Two CTAs
 // share an SM.  Per chunk:
 //   chain group (warps 4-7)   S -> K S -> W -> T W = U -> K^T diag(tail) U -> S: three products,
-//                             each waiting for the last, and nothing else;
-//   output group (warps 0-3)  Q K^T and P a chunk ahead, scale diag(gamma) Q S + P U, the output;
-//   issuer (warp 8)           all products but Q K^T: issuing four takes some 150 cycles, which a
-//                             warp of the chain would be late with its share of the next step;
-//   loader (warp 9)           the copies of later chunks.
+//                             each waiting for the last.  One warp issues them, another the copies
+//                             of later chunks, both while the group waits for a product anyway;
+//   output group (warps 0-3)  Q K^T and P a chunk ahead, scale diag(gamma) Q S + P U, the output.
 //
 // Accuracy.  The state is an fp32 result, so every operand between S and the next S is two bf16
 // terms, hi and lo (K and V are exact): S, W, T and diag(tail) U, three products where both
@@ -38,7 +36,7 @@ namespace wkv {
 namespace {
 using namespace dtc;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 256;
 constexpr int OFF_K = 0, OFF_Q = 2 * kTile, OFF_V = 4 * kTile, OFF_P = 5 * kTile, OFF_T = 6 * kTile;
 constexpr int OFF_A = 10 * kTile, OFF_B = 11 * kTile, OFF_CC = 12 * kTile;
 constexpr int OFF_DEC = 13 * kTile;                               // Decays
@@ -84,32 +82,31 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const uint32_t bar_x = smem_u32(&bars[8]);    // K S, U, K^T U done (three phases a chunk)
     const uint32_t bar_qs = smem_u32(&bars[9]);   // Q S done
     const uint32_t bar_o = smem_u32(&bars[10]);   // P U done
-    const uint32_t bar_p = smem_u32(&bars[11]);   // P written, Q S scaled
-    const uint32_t bar_sr = smem_u32(&bars[12]);  // Q K^T read: its columns may take Q S
-    const uint32_t bar_tf = smem_u32(&bars[13]);  // U done: V and T have been read
-    const uint32_t bar_kf0 = smem_u32(&bars[14]); // K^T U done: K and Q have been read, + 8 * (chunk % 2)
-    const uint32_t bar_r = smem_u32(&bars[16]);   // S, W, U written (three phases a chunk)
+    const uint32_t bar_sw = smem_u32(&bars[13]);  // S, U written
+    const uint32_t bar_uw = smem_u32(&bars[16]);
     const uint32_t bar_never = smem_u32(&bars[17]);
-    // decays written, tail rows of K and Q zeroed: + 8 * (chunk % 3)
+    // decays written: + 8 * (chunk % 3), since the output group may pass two more chunks here before the
+    // chain waits for this one
     const uint32_t bar_s0 = smem_u32(&bars[18]);
     const uint32_t bar_drain = smem_u32(&bars[21]);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, see elect_one
     const int64_t n = blockIdx.x, seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
-    int64_t first, len;
-    sequence_span(p.offsets, seq, p.T, &first, &len);
+    int64_t first_, len_;
+    sequence_span(p.offsets, seq, p.T, &first_, &len_);
+    const int first = static_cast<int>(first_), len = static_cast<int>(len_);  // fewer than 2^31 tokens in all
     const int64_t slot = sequence_slot(p.slots, seq, p.nslots, tid == 0 ? p.status : nullptr);
-    const int nchunks = static_cast<int>((len + kC - 1) / kC);
+    const int nchunks = (len + kC - 1) / kC;
     const int64_t chunk0 = first_chunk(p.offsets != nullptr, seq, first, p.T);
     // tensor-map coordinates of the sequence's first token
-    const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = p.offsets ? static_cast<int>(first) : 0;
+    const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = p.offsets ? first : 0;
     const uint32_t spin = p.spin_limit;
     const int64_t ntok = p.B * p.T;
 
     if (tid == 0) {
         for (int i = 0; i < 22; ++i)
-            bar_init(smem_u32(&bars[i]), i == 11 || i == 12 || i == 16 ? 128 : i == 21 ? 2 : i > 17 ? 65 : 1);
+            bar_init(smem_u32(&bars[i]), i == 21 ? 3 : i > 17 ? 64 : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         misc[1] = 0;
     }
@@ -119,8 +116,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    // P and T are lower triangular: the blocks above the diagonal are zeroed once
-    for (int i = tid; i < 5 * kTile / 16; i += kThreads)
+    // P is lower triangular: the blocks above the diagonal are zeroed once
+    for (int i = tid; i < kTile / 16; i += kThreads)
         *reinterpret_cast<uint4 *>(sm + OFF_P + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
     fence_before();
@@ -133,28 +130,21 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         bar_expect_tx(bar, kTile);
         tma_load_4d(smem_u32(sm + off), map, 0, static_cast<int>(head), row_t + c * kC, row_b, bar);
     };
-    // T of chunk c, without its zero blocks: one warp, a copy for each of 8 core columns of each term
-    auto load_t = [&](int c) {
+    auto load_t = [&](int c) {  // one thread
         if (!in_bounds(p.status, chunk0 + c, 1, p.nchunks)) return;
         const uint32_t bar = bar_t0 + 8 * (c & 1);
-        if (lane == 0) bar_expect_tx(bar, kTBytes);
-        __syncwarp();
-        if (lane < 16) {
-            const int col = lane & 7, term = lane >> 3;
-            bulk_load(smem_u32(sm + OFF_T + kTile * (2 * (c & 1) + term) + 1024 * col + 256 * (col >> 1)),
-                      p.t + ((chunk0 + c) * p.H + h) * kTBytes + term * kTStored + t_stored_at(col),
-                      (8 - 2 * (col >> 1)) * 128, bar);
-        }
+        bar_expect_tx(bar, kTBytes);
+        bulk_load(smem_u32(sm + OFF_T + kTBytes * (c & 1)), p.t + ((chunk0 + c) * p.H + h) * kTBytes, kTBytes, bar);
     };
-    if (warp == 9) {
+    if (warp == 7) {
         for (int c = 0; c < 2 && c < nchunks; ++c) {
             if (elect_one()) {
                 load_tile(&map_k, OFF_K + kTile * c, hk, c, bar_k0 + 8 * c);
                 if (!STATES) load_tile(&map_q, OFF_Q + kTile * c, hk, c, bar_q0 + 8 * c);
                 if (c < 1) load_tile(&map_v, OFF_V, h, c, bar_v);
+                load_t(c);
             }
             __syncwarp();
-            load_t(c);
         }
     }
     int abort = 0;
@@ -162,102 +152,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     abort = __syncthreads_or(abort);
     if (abort) misc[1] = 1;
 
-    if (warp == 8) {
-        // ---------------------------------------------------------------------- issuer
-        const uint32_t tA = smem_u32(sm + OFF_A), tB = smem_u32(sm + OFF_B), tC = smem_u32(sm + OFF_CC);
-        const uint64_t dA = desc_mn(tA), dB = desc_mn(tB), dC = desc_mn(tC), dP = desc_k(smem_u32(sm + OFF_P));
-        constexpr uint32_t kId = idesc(64, 0, 1), kId2 = idesc(128, 0, 1), kIdT2 = idesc(128, 1, 1);
-        uint32_t rph = 0;
-        int ok = !abort;
-        for (int c = 0; c < nchunks && ok; ++c) {
-            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (c & 1)), aT = smem_u32(sm + OFF_T + 2 * kTile * (c & 1));
-            const uint64_t dK = desc_k(aK), dKt = desc_mn(aK), dQ = desc_k(smem_u32(sm + OFF_Q + kTile * (c & 1)));
-            const uint64_t dTh = desc_t(aT), dTl = desc_t(aT + kTile);
-            const uint32_t co = tbase + COL_O + 64 * (c & 1);
-            auto wait = [&](uint32_t bar, uint32_t phase) {
-                if (ok) ok = __all_sync(0xffffffffu, bar_wait_spin(bar, phase, spin * 64u));
-                fence_after();
-            };
-            wait(bar_s0 + 8 * (c % 3), (c / 3) & 1);
-            wait(bar_r, rph);  // S
-            rph ^= 1;
-            const int64_t tile = ((chunk0 + c) * p.H + h) * kTile;
-            if (STATES && ok && lane == 0 && in_bounds(p.status, chunk0 + c, 1, p.nchunks)) {
-                bulk_store(p.states + tile, tA, kTile);
-                bulk_commit();
-            }
-            if (ok && elect_one()) {  // K S
-                mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, kId2);
-                mma_commit(bar_x);
-            }
-            __syncwarp();
-            if (!STATES) wait(bar_sr, c & 1);
-            if (STATES && lane == 0) {  // the copy of S has read it
-                bulk_wait_read<0>();
-                bar_arrive(bar_qs);
-            }
-            if (!STATES && ok && elect_one()) {  // Q S
-                mma_tile<kStepK, kStepMn, false>(co, dQ, dA, kId);
-                mma_commit(bar_qs);
-            }
-            __syncwarp();
-            wait(bar_t0 + 8 * (c & 1), (c >> 1) & 1);
-            wait(bar_r, rph);  // W
-            rph ^= 1;
-            if (ok && elect_one()) {  // U = T W
-                mma_tile<kStepTK, kStepMn, false>(tbase + COL_X, dTh, dB, kId2);
-                mma_tile<kStepTK, kStepMn, true>(tbase + COL_X, dTl, dB, kId);
-                mma_commit(bar_x);
-                mma_commit(bar_tf);
-            }
-            __syncwarp();
-            wait(bar_r, rph);  // U
-            rph ^= 1;
-            if (STATES && ok && lane == 0 && in_bounds(p.status, chunk0 + c, 1, p.nchunks)) {
-                bulk_store(p.us + tile, tC, kTile);
-                bulk_commit();
-            }
-            if (ok && elect_one()) {  // K^T diag(tail) U
-                mma_tile<kStepMn, kStepMn, false>(tbase + COL_X, dKt, dA, kIdT2);
-                mma_commit(bar_x);
-                mma_commit(bar_kf0 + 8 * (c & 1));  // and Q S before it
-            }
-            __syncwarp();
-            if (!STATES) wait(bar_p, c & 1);
-            if (STATES && lane == 0) {  // the copy of U has read it
-                bulk_wait_read<0>();
-                bar_arrive(bar_o);
-            }
-            if (!STATES && ok && elect_one()) {  // + P U
-                mma_tile<kStepK, kStepMn, true>(co, dP, dC, kId);
-                mma_commit(bar_o);
-            }
-            __syncwarp();
-        }
-        if (STATES && lane == 0) bulk_wait_all();
-        if (!ok) misc[1] = 1;
-    } else if (warp == 9) {
-        // ---------------------------------------------------------------------- loader
-        // A wait by parity must not be two phases late.  The chain cannot reach U of chunk c + 1
-        // before V of c + 1, which is loaded after the wait for U of c; nor K^T U of c + 2 before
-        // K of c + 2, loaded after the wait for K^T U of c (whose barriers alternate).
-        int ok = 1;
-        for (int c = 0; c + 1 < nchunks && !abort && ok; ++c) {
-            ok = __all_sync(0xffffffffu, bar_wait(bar_tf, c & 1, spin));
-            if (!ok) break;
-            if (elect_one()) load_tile(&map_v, OFF_V, h, c + 1, bar_v);
-            __syncwarp();
-            if (c + 2 >= nchunks) break;
-            load_t(c + 2);
-            ok = __all_sync(0xffffffffu, bar_wait(bar_kf0 + 8 * (c & 1), (c >> 1) & 1, spin));
-            if (ok && elect_one()) {
-                load_tile(&map_k, OFF_K + kTile * (c & 1), hk, c + 2, bar_k0 + 8 * (c & 1));
-                if (!STATES) load_tile(&map_q, OFF_Q + kTile * (c & 1), hk, c + 2, bar_q0 + 8 * (c & 1));
-            }
-            __syncwarp();
-        }
-        if (!ok) misc[1] = 1;
-    } else if (warp < 4) {
+    if (warp < 4) {
         // ---------------------------------------------------------------- output group
         const int w = warp;
         Decays &dec = *reinterpret_cast<Decays *>(sm + OFF_DEC);
@@ -267,10 +162,10 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const int st = tid - 64;
         uint16_t g_next = 0, b_next = 0;
         auto fetch = [&](int c) {
-            const int64_t t = static_cast<int64_t>(c) * kC + st;
+            const int t = c * kC + st;
             g_next = b_next = 0;
             if (t >= len || !in_bounds(p.status, first + t, 1, ntok)) return;
-            const int64_t at = (first + t) * p.H + h;
+            const int64_t at = static_cast<int64_t>(first + t) * p.H + h;
             g_next = reinterpret_cast<const uint16_t *>(p.g)[at];
             b_next = reinterpret_cast<const uint16_t *>(p.beta)[at];
         };
@@ -280,29 +175,18 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             scan_decays<3>(dec, arrays[c % 3], st, gv, bv);
             bar_arrive(bar_s0 + 8 * (c % 3));
         };
-        // Q K^T of chunk c (warp 0)
+        // Q K^T of chunk c (warp 0).  Rows past the sequence's end hold another's tokens; they stay in
+        // rows of P that are not stored and in columns that the mask takes out.
         auto products = [&](int c) -> int {
-            unsigned char *kt = sm + OFF_K + kTile * (c & 1), *qt = sm + OFF_Q + kTile * (c & 1);
+            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (c & 1)), aQ = smem_u32(sm + OFF_Q + kTile * (c & 1));
             const bool there = bar_wait(bar_k0 + 8 * (c & 1), (c >> 1) & 1, spin) &&
-                               (STATES || bar_wait(bar_q0 + 8 * (c & 1), (c >> 1) & 1, spin));
+                               bar_wait(bar_q0 + 8 * (c & 1), (c >> 1) & 1, spin);
             if (!__all_sync(0xffffffffu, there)) return 0;
-            const int64_t left = len - static_cast<int64_t>(c) * kC;
-            if (left < kC) {
-                zero_rows(kt, static_cast<int>(left), lane, 32);
-                if (!STATES) zero_rows(qt, static_cast<int>(left), lane, 32);
-                fence_async_smem();
-                __syncwarp();
-            }
-            if (STATES) {
-                if (lane == 0) bar_arrive(bar_s0 + 8 * (c % 3));
-                return 1;
-            }
             fence_after();
-            const uint64_t dk = desc_k(smem_u32(kt)), dq = desc_k(smem_u32(qt));
+            const uint64_t dk = desc_k(aK), dq = desc_k(aQ);
             if (elect_one()) {
                 mma_tile<kStepK, kStepK, false>(tbase + COL_O + 64 * (c & 1), dq, dk, idesc(64, 0, 0));
                 mma_commit(bar_a);
-                bar_arrive(bar_s0 + 8 * (c % 3));
             }
             __syncwarp();
             return 1;
@@ -312,49 +196,52 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         auto store_o = [&](int c) {  // output rows of chunk c
             P2 x[16];
             tmem_ld_row(co + 64 * (c & 1), x);
-            const int64_t tok = static_cast<int64_t>(c) * kC + row;
+            const int tok = c * kC + row;
             if (tok < len && in_bounds(p.status, first + tok, 1, ntok)) {
-                uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((first + tok) * p.H + h) * kN + col);
+                uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(first + tok) * p.H + h) * kN + col);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     dst[i] = make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
             }
         };
         int ok = 1;
+        uint32_t ph[4][4], pl[4][4];  // P of the next chunk to store; pl: unused
         if (!abort && nchunks > 0) {
             if (w >= 2) {
                 fetch(0);
                 scan(0);
-            } else if (w == 0) {
-                ok = products(0);
+            }
+            if (!STATES) {
+                if (w == 0) ok = products(0);
+                group_sync<1, 128>();
+                if (ok) ok = bar_wait(bar_a, 0, spin);
+                fence_after();
+                form_p<false>(dec, w, lane, co, p.scale, ph, pl);
+                fence_before();
             }
         }
         for (int c = 0; c < nchunks && !abort; ++c) {
-            group_sync<1, 128>();  // the chunk's decays are there
-            if (STATES) {  // nothing but the next chunk's decays and tail rows
-                if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);
-                if (named_sync_or(1, 128, !ok || misc[1])) {
-                    abort = 1;
-                    misc[1] = 1;
-                    break;
-                }
-                if (c + 1 < nchunks) {
-                    if (w >= 2) scan(c + 1);
-                    else if (w == 0) ok = products(c + 1);
-                }
-                continue;
-            }
-            if (ok) ok = bar_wait(bar_a, c & 1, spin);
-            fence_after();
-            uint32_t ph[4][4], pl[4][4];  // pl: unused
-            form_p<false>(dec, w, lane, co + 64 * (c & 1), p.scale, ph, pl, [&] {
-                fence_before();
-                bar_arrive(bar_sr);
-            });
-            if (named_sync_or(1, 128, !ok || misc[1])) {
+            if (named_sync_or(1, 128, !ok || misc[1])) {  // Q K^T and the decays have been read
                 abort = 1;
                 misc[1] = 1;
                 break;
+            }
+            if (STATES) {  // nothing but the next chunk's decays
+                if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);
+                if (w >= 2 && c + 1 < nchunks) scan(c + 1);
+                continue;
+            }
+            const uint32_t dst = tbase + COL_O + 64 * (c & 1);
+            if (w == 1) {  // Q S, once S is written
+                if (ok) ok = bar_wait(bar_sw, c & 1, spin);
+                fence_after();
+                __syncwarp();
+                const uint64_t dQ = desc_k(smem_u32(sm + OFF_Q + kTile * (c & 1))), dS = desc_mn(smem_u32(sm + OFF_A));
+                if (elect_one()) {
+                    mma_tile<kStepK, kStepMn, false>(dst, dQ, dS, idesc(64, 0, 1));
+                    mma_commit(bar_qs);
+                }
+                __syncwarp();
             }
             if (w >= 2 && c + 1 < nchunks) scan(c + 1);
             if (c > 0) {
@@ -366,9 +253,6 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 if (j <= w) st_block(sm + OFF_P, w, j, lane, ph[j]);
             fence_async_smem();
             if (c > 0) store_o(c - 1);
-            fence_before();
-            group_sync<1, 128>();
-            if (w == 0 && c + 1 < nchunks && !products(c + 1)) ok = 0;
             // scale diag(gamma) Q S, in place
             if (ok) ok = bar_wait(bar_qs, c & 1, spin);
             fence_after();
@@ -381,14 +265,32 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 tmem_st32(co + 64 * (c & 1), v);
             }
             fence_before();
-            bar_arrive(bar_p);
+            group_sync<1, 128>();
+            if (c + 1 < nchunks) {
+                if (w == 0 && !products(c + 1)) ok = 0;
+                if (ok) ok = bar_wait(bar_a, (c + 1) & 1, spin);
+                fence_after();
+                form_p<false>(dec, w, lane, co + 64 * ((c + 1) & 1), p.scale, ph, pl);
+                fence_before();
+            }
+            if (w == 1) {  // + P U
+                if (ok) ok = bar_wait(bar_uw, c & 1, spin);
+                fence_after();
+                __syncwarp();
+                const uint64_t dP = desc_k(smem_u32(sm + OFF_P)), dU = desc_mn(smem_u32(sm + OFF_CC));
+                if (elect_one()) {
+                    mma_tile<kStepK, kStepMn, true>(dst, dP, dU, idesc(64, 0, 1));
+                    mma_commit(bar_o);
+                }
+                __syncwarp();
+            }
         }
         if (!STATES && !abort && nchunks > 0) {
             if (ok) ok = bar_wait(bar_o, (nchunks - 1) & 1, spin);
             fence_after();
             if (ok) store_o(nchunks - 1);
-            else misc[1] = 1;
         }
+        if (!ok) misc[1] = 1;
     } else {
         // ------------------------------------------------------------------ chain group
         const int q = warp & 3;
@@ -410,9 +312,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i] = pk(0.f, 0.f);
         }
-        uint32_t at[4];  // this thread's 32 columns of a tile
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = swz(row, 2 * col + 16 * i);
+        const uint32_t at0 = swz(row, 2 * col);  // this thread's 32 columns of a tile: i-th 16 bytes
+        auto at = [&](int i) { return at0 ^ static_cast<uint32_t>(16 * i); };
         // half of them (16 columns) as two bf16 terms
         auto store_split = [&](const P2 *x, int half, unsigned char *th, unsigned char *tlo) {
 #pragma unroll
@@ -420,35 +321,72 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 uint32_t a[4], b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split2(x[4 * i + e], &a[e], &b[e]);
-                *reinterpret_cast<uint4 *>(th + at[2 * half + i]) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4 *>(tlo + at[2 * half + i]) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4 *>(th + at(2 * half + i)) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4 *>(tlo + at(2 * half + i)) = make_uint4(b[0], b[1], b[2], b[3]);
             }
         };
-        // what was written is ready for the issuer, what was read may be written again
-        auto ready = [&]() {
+        const uint64_t dA = desc_mn(smem_u32(tA)), dB = desc_mn(smem_u32(tB));
+        constexpr uint32_t kId = idesc(64, 0, 1), kId2 = idesc(128, 0, 1), kIdT2 = idesc(128, 1, 1);
+        // group barrier: what was written is ready for the products issued next
+        auto meet = [&]() {
             fence_async_smem();
             fence_before();
-            bar_arrive(bar_r);
+            group_sync<2, 128>();
+            fence_after();
         };
         uint32_t xph = 0;  // phase of bar_x
         int ok = !abort;
-        for (int c = 0; c < nchunks; ++c) {
-            if (!__all_sync(0xffffffffu, ok)) break;  // a wait ran out
-            // ---- S hi, lo
+        for (int c = 0; c < nchunks && !abort; ++c) {
+            const uint32_t aK = smem_u32(sm + OFF_K + kTile * (c & 1));
+            const int64_t tile = ((chunk0 + c) * p.H + h) * kTile;
+            // ---- S hi, lo; K S.  Whether to stop is voted on here (an expired wait makes the rest of its
+            // chunk's waits pass)
             store_split(S, 0, tA, tB);
             store_split(S + 8, 1, tA, tB);
-            ready();
+            if (ok) ok = bar_wait(bar_s0 + 8 * (c % 3), (c / 3) & 1, spin);
+            if (ok) ok = bar_wait(bar_k0 + 8 * (c & 1), (c >> 1) & 1, spin);
+            if (c * kC + kC > len) zero_rows(sm + OFF_K + kTile * (c & 1), len - c * kC, tid - 128, 128);
+            fence_async_smem();
+            fence_before();
+            if (named_sync_or(2, 128, !ok || misc[1])) {
+                abort = 1;
+                break;
+            }
+            fence_after();
+            if (warp == 4) {
+                const uint64_t dK = desc_k(aK);
+                if (elect_one()) {
+                    mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, kId2);
+                    mma_commit(bar_x);
+                }
+                __syncwarp();
+            } else if (warp == 5 && lane == 0) {
+                if (!STATES) {
+                    bar_arrive(bar_sw);
+                } else {
+                    if (in_bounds(p.status, chunk0 + c, 1, p.nchunks)) bulk_store(p.states + tile, smem_u32(tA), kTile);
+                    bulk_commit();
+                    bulk_wait_read<0>();
+                    bar_arrive(bar_qs);
+                }
+            } else if (warp == 7 && c > 0 && c + 1 < nchunks) {  // S is there: the chunk before is done with its tiles
+                if (elect_one()) {
+                    load_tile(&map_k, OFF_K + kTile * ((c + 1) & 1), hk, c + 1, bar_k0 + 8 * ((c + 1) & 1));
+                    if (!STATES) load_tile(&map_q, OFF_Q + kTile * ((c + 1) & 1), hk, c + 1, bar_q0 + 8 * ((c + 1) & 1));
+                }
+            }
+            __syncwarp();
             // ---- W = beta (v - gamma K S)
-            ok = bar_wait(bar_s0 + 8 * (c % 3), (c / 3) & 1, spin);
             const ChunkArrays &arr = reinterpret_cast<const ChunkArrays *>(sm + OFF_ARR)[c % 3];
             const float gam = arr.gamma[row], tail = arr.tail[row], bet = arr.beta[row], gC = arr.gamma[kC - 1];
             const P2 b2 = pk(bet, bet), bg = pk(-bet * gam, -bet * gam), t2 = pk(tail, tail), g2 = pk(gC, gC);
             if (ok) ok = bar_wait(bar_v, c & 1, spin);
             if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);  // P U has read U
+            if (ok) ok = bar_wait(bar_t0 + 8 * (c & 1), (c >> 1) & 1, spin);
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
-            const bool token = static_cast<int64_t>(c) * kC + row < len;  // else another sequence's, or nothing
+            const bool token = c * kC + row < len;  // else another sequence's, or nothing
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 P2 x[8];
@@ -456,14 +394,27 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint4 vv = make_uint4(0u, 0u, 0u, 0u);
-                    if (token) vv = *reinterpret_cast<const uint4 *>(sm + OFF_V + at[2 * half + i]);
+                    if (token) vv = *reinterpret_cast<const uint4 *>(sm + OFF_V + at(2 * half + i));
                     const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[4 * i + e] = fma2(bg, x[4 * i + e], mul2(b2, unpack2(vw[e])));
                 }
                 store_split(x, half, tB, tC);
             }
-            ready();
+            meet();
+            if (warp == 4) {  // ---- U = T W
+                const uint32_t aT = smem_u32(sm + OFF_T + 2 * kTile * (c & 1));
+                const uint64_t dTh = desc_t(aT), dTl = desc_t(aT + kTile);
+                if (elect_one()) {
+                    mma_tile<kStepTK, kStepMn, false>(tbase + COL_X, dTh, dB, kId2);
+                    mma_tile<kStepTK, kStepMn, true>(tbase + COL_X, dTl, dB, kId);
+                    mma_commit(bar_x);
+                }
+                __syncwarp();
+            } else if (warp == 7 && c + 1 < nchunks) {
+                if (elect_one()) load_tile(&map_v, OFF_V, h, c + 1, bar_v);
+                __syncwarp();
+            }
             // ---- U, and diag(tail) U hi, lo
             if (ok) ok = bar_wait(bar_qs, c & 1, spin);  // Q S has read S
             if (ok) ok = bar_wait(bar_x, xph, spin);
@@ -475,13 +426,33 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 tmem_ld_sum16(tl + COL_X + 16 * half, x);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4 *>(tC + at[2 * half + i]) =
+                    *reinterpret_cast<uint4 *>(tC + at(2 * half + i)) =
                         make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], t2);
                 store_split(x, half, tA, tB);
             }
-            ready();
+            meet();
+            if (warp == 4) {  // ---- K^T diag(tail) U
+                const uint64_t dKt = desc_mn(aK);
+                if (elect_one()) {
+                    mma_tile<kStepMn, kStepMn, false>(tbase + COL_X, dKt, dA, kIdT2);
+                    mma_commit(bar_x);
+                }
+                __syncwarp();
+            } else if (warp == 5 && lane == 0) {
+                if (!STATES) {
+                    bar_arrive(bar_uw);
+                } else {
+                    if (in_bounds(p.status, chunk0 + c, 1, p.nchunks)) bulk_store(p.us + tile, smem_u32(tC), kTile);
+                    bulk_commit();
+                    bulk_wait_read<0>();
+                    bar_arrive(bar_o);
+                }
+            } else if (warp == 7 && c + 2 < nchunks) {
+                if (elect_one()) load_t(c + 2);
+            }
+            __syncwarp();
             // ---- S
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
@@ -494,6 +465,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 for (int i = 0; i < 8; ++i) S[8 * half + i] = fma2(g2, S[8 * half + i], x[i]);
             }
         }
+        if (STATES && warp == 5 && lane == 0) bulk_wait_all();
+        if (abort) ok = 0;
         if (!ok) misc[1] = 1;
         if (ok && p.sT && slot >= 0 && in_bounds(p.status, sat, 32, nstate)) {
             float4 *dst = reinterpret_cast<float4 *>(p.sT + sat);
@@ -508,7 +481,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     fence_after();
     if (abort) {
         record_status(p.status, kStatusTimeout);
-        if ((warp == 0 || warp == 8) && elect_one()) mma_commit(bar_drain);  // the two issuers
+        if ((warp == 0 || warp == 1 || warp == 4) && elect_one()) mma_commit(bar_drain);  // the issuers
         if (tid == 0) {
             bar_wait(bar_drain, 0, p.spin_limit);
             for (int i = 0; i < 7; ++i)  // copies in flight: a barrier that nothing will complete runs out

@@ -16,8 +16,8 @@
 //           with both operands split into two bf16 terms, hi and lo, three products each (the
 //           error left is that of lo, 2^-16): T enters the fp32 state.
 //
-// T is written as its two terms, without the zero blocks, in the order in which the walking kernels
-// hold it in shared memory; a warp's store is one 128-byte line.
+// T is written as its two terms in the order in which the walking kernels hold it in shared memory;
+// a warp's store is one 128-byte line.
 #include "delta_tc.cuh"
 
 namespace wkv {
@@ -299,11 +299,20 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     auto put = [&](int i, int j, const Frag &f) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            unsigned char *at = tout + t_stored_at(2 * j + (q >> 1)) + (2 * (i - j) + (q & 1)) * 128 + 4 * lane;
+            unsigned char *at = tout + (2 * j + (q >> 1)) * 1024 + (2 * i + (q & 1)) * 128 + 4 * lane;
             *reinterpret_cast<uint32_t *>(at) = f.h[q];
-            *reinterpret_cast<uint32_t *>(at + kTStored) = f.l[q];
+            *reinterpret_cast<uint32_t *>(at + kTile) = f.l[q];
         }
     };
+    if (tid < 96) {  // the blocks above the diagonal: core columns 2 .. 7, the rows above 16 (c / 2)
+        const int c = 2 + tid / 16, at = 1024 * c + 16 * (tid % 16);
+#pragma unroll
+        for (int r = 0; r < 3; ++r)
+            if (r < c / 2) {
+                *reinterpret_cast<uint4 *>(tout + at + 256 * r) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(tout + kTile + at + 256 * r) = make_uint4(0u, 0u, 0u, 0u);
+            }
+    }
     if (w == 0) {
         const Frag d0 = D(0), d1 = D(1), l10 = L(1, 0), a1 = turn(d1);
         const Frag t10 = times(times(a1, l10, 1.f), d0, -1.f);

@@ -53,12 +53,11 @@ __device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uin
     for (uint32_t ks = 0; ks < 4; ++ks) mma(d, a + SA * ks, b + SB * ks, id, ACC || ks > 0);
 }
 
-// T as an operand in shared memory: 8 x 8 core matrices of 128 bytes (8 rows of 16 bytes), core
-// (r, c) of rows 8 r .., columns 8 c .. at 1024 c + 128 r, no swizzle.  That order lets the blocks
-// above the diagonal, which are zero, be left out of what is stored and copied: column c holds
-// the rows from 16 (c / 2) on.
-constexpr int kTStored = 5120;             // bytes of one of T's two terms as stored: hi, then lo
-constexpr int kTBytes = 2 * kTStored;      // per chunk and head
+// T as an operand: 8 x 8 core matrices of 128 bytes (8 rows of 16 bytes), core (r, c) of rows 8 r ..,
+// columns 8 c .. at 1024 c + 128 r, no swizzle; hi, then lo.  It is stored as it lies in shared
+// memory, zero blocks included: one copy of 16 KB.  (Leaving the zeros out saves 6 KB a chunk but
+// takes 16 copies, which hold the warp that issues them for some 1000 cycles.)
+constexpr int kTBytes = 2 * kTile;  // per chunk and head
 constexpr uint32_t kStepTK = 2 * 1024 / 16, kStepTMn = 2 * 128 / 16;
 __device__ __forceinline__ uint64_t udesc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo)
 {
@@ -69,12 +68,6 @@ __device__ __forceinline__ uint64_t udesc_plain(uint32_t addr, uint32_t lbo, uin
 __device__ __forceinline__ uint64_t desc_t(uint32_t addr) { return udesc_plain(addr, 1024, 128); }
 // read across them (T^T dU): K steps of 16 rows are 256 bytes
 __device__ __forceinline__ uint64_t desc_tt(uint32_t addr) { return udesc_plain(addr, 128, 1024); }
-__host__ __device__ constexpr int t_stored_at(int c)  // byte offset of core column c in a stored term
-{
-    return 256 * (8 * (c / 2) - (c / 2) * (c / 2 - 1)) + (c & 1) * (8 - 2 * (c / 2)) * 128;
-}
-static_assert(t_stored_at(7) + 256 == kTStored, "stored blocks of T");
-
 // Chunks of a call are numbered through: sequences take disjoint runs, since each needs at most
 // one more than its share of the tokens.
 __host__ __device__ __forceinline__ int64_t first_chunk(bool packed, int64_t seq, int64_t first, int64_t T)
@@ -239,10 +232,9 @@ __device__ __forceinline__ float widen(uint16_t bf16) { return __uint_as_float(s
 
 // Block row w of P from Q K^T in tensor memory (this warp's lanes), as bf16 pairs in the layout of
 // mma.sync accumulators; pl: what ph leaves, with LO.  Blocks right of the diagonal are zero.
-// `read` is called once the products have been read.
-template <bool LO, typename F>
+template <bool LO>
 __device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_t qk, float scale, uint32_t (&ph)[4][4],
-                                       uint32_t (&pl)[4][4], F read)
+                                       uint32_t (&pl)[4][4])
 {
     const int g = lane >> 2, t = lane & 3, r0 = 16 * w + g;
     const float n0 = d.pn[r0], n1 = d.pn[r0 + 8], f0 = d.pf[r0], f1 = d.pf[r0 + 8];
@@ -260,7 +252,6 @@ __device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 8; ++i) after_wait(x[i >> 2][i & 3]);
-        if (j == 0) read();
         const float mid = ex2_approx(mn + mf);
         if (j < w) mn += d.bs[j], mf += d.bs[4 + j];
 #pragma unroll
@@ -273,7 +264,7 @@ __device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_
                 for (int r = 0; r < 2; ++r) {
                     const float e0 = ex2_approx(((r ? n1 : n0) - tc::lo(cn)) + ((r ? f1 : f0) - tc::lo(ff)));
                     const float e1 = ex2_approx(((r ? n1 : n0) - tc::hi(cn)) + ((r ? f1 : f0) - tc::hi(ff)));
-                    gam[r] = pk(col <= g + 8 * r ? scale * e0 : 0.f, col + 1 <= g + 8 * r ? scale * e1 : 0.f);
+                    gam[r] = pk(scale * e0, scale * e1);
                 }
             } else {
                 const P2 cc = ld_p2(d.cf + 16 * j + 8 * nn + 2 * t);
@@ -285,7 +276,11 @@ __device__ __forceinline__ void form_p(const Decays &d, int w, int lane, uint32_
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const P2 y = mul2(gam[r], pk(x[nn][2 * r], x[nn][2 * r + 1]));
+                P2 y = mul2(gam[r], pk(x[nn][2 * r], x[nn][2 * r + 1]));
+                if (j == w) {  // masked by choice, not by a zero factor: there may be no number there
+                    const int col = 8 * nn + 2 * t;
+                    y = pk(col <= g + 8 * r ? tc::lo(y) : 0.f, col + 1 <= g + 8 * r ? tc::hi(y) : 0.f);
+                }
                 if (LO) split2(y, &ph[j][2 * nn + r], &pl[j][2 * nn + r]);
                 else ph[j][2 * nn + r] = pack2(y);
             }
