@@ -9,7 +9,7 @@
 //
 //   L       warp w forms block column w of L from the blocks of K K^T right of the diagonal in block
 //           row w (K K^T is symmetric), which puts L in the register order of a B operand.
-//   D[w]    inverse of the diagonal block by substitution in fp32, a column per lane.
+//   D[w]    inverse of the diagonal block by substitution in fp32, a column per lane, two blocks a warp.
 //   T       T10 = -(D1 L10) D0              T21 = -Z D1, Z = D2 L21     T20 = -(D2 L20 D0 + Z T10)
 //           T32 = -(D3 L32) D2              T31 = -Y D1, Y = D3 L31 + T32 L21
 //           T30 = -((D3 L30 + T32 L20) D0 + Y T10)
@@ -242,12 +242,13 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
             put_block(sm + OFF_L + 1024 * (j * (j - 1) / 2 + w), lane, f);
         }
     }
-    __syncwarp();
-    // ---- D[w]: column (lane % 16) by substitution in registers, the next column of L loading under
-    // the current one's updates
-    {
-        const float4 *xt = reinterpret_cast<const float4 *>(sm + OFF_X + 1024 * w);
-        const int j = lane & 15;
+    __syncthreads();
+    // ---- D: warps 2 and 3 (which had the least of L to form), a block in each half-warp, a column in
+    // each lane, by substitution in registers; the next column of L loads under the current one's
+    // updates
+    if (w >= 2) {
+        const int blk = 2 * (w - 2) + (lane >> 4), j = lane & 15;
+        const float4 *xt = reinterpret_cast<const float4 *>(sm + OFF_X + 1024 * blk);
         P2 x[8], la[8], lb[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = pk(2 * i == j ? 1.f : 0.f, 2 * i + 1 == j ? 1.f : 0.f);
@@ -274,18 +275,16 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
             if (k + 2 < 15) fetch(k + 2, la);
             if (k + 1 < 15) update(k + 1, lb);
         }
-        uint32_t out[8];
-        const bool is_lo = lane >= 16;  // these lanes hold the same columns and write the lo terms
+        uint32_t dh[8], dl[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t hh, ll;
-            split2(x[i], &hh, &ll);
-            out[i] = is_lo ? ll : hh;
-        }
+        for (int i = 0; i < 8; ++i) split2(x[i], &dh[i], &dl[i]);
         __syncwarp();
-        unsigned char *at = sm + OFF_X + 1024 * w + (is_lo ? 512 : 0) + 64 * (j & 7) + 8 * (j >> 3);
+        unsigned char *at = sm + OFF_X + 1024 * blk + 64 * (j & 7) + 8 * (j >> 3);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint2 *>(at + 16 * q) = make_uint2(out[q], out[4 + q]);
+        for (int q = 0; q < 4; ++q) {
+            *reinterpret_cast<uint2 *>(at + 16 * q) = make_uint2(dh[q], dh[4 + q]);
+            *reinterpret_cast<uint2 *>(at + 512 + 16 * q) = make_uint2(dl[q], dl[4 + q]);
+        }
     }
     if (__syncthreads_or(!ok)) {
         if (tid == 0) record_status(p.status, kStatusTimeout);
