@@ -14,6 +14,7 @@ The calls are asynchronous on torch's current CUDA stream.
 """
 import contextlib
 import ctypes
+import functools
 import os
 import re
 
@@ -362,18 +363,34 @@ def wkv6_backward(r, k, v, w, u, dy, s0=None, dsT=None, omega=False, want_ds0=Tr
     return out
 
 
-@contextlib.contextmanager
-def _on_device_of(lib, t):
-    """The tensor's device made current, its current torch stream the library's."""
-    with torch.cuda.device(t.device):
-        _use_current_stream(lib, t.device)
-        yield
+def _call(lib, device, fn, *args):
+    """fn(*args) on the tensors' device and its current torch stream; raises on an error status."""
+    index = device.index
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _call(lib, device, fn, *args)
+    lib.rwkv_set_stream(torch._C._cuda_getCurrentRawStream(index))
+    _check(fn(*args))
 
 
-def _same_device(t, **others):
-    for name, x in others.items():
-        if x is not None and x.device != t.device:
-            raise ValueError(f"{name} is on {x.device}, not on {t.device}")
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _tensor(t, name, dtype, shape, device):
+    """Like _cuda, for the operators whose calls take microseconds: one pass over what is usual."""
+    if t is None:
+        return
+    if (t.__class__ is not torch.Tensor and not isinstance(t, torch.Tensor)) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _delta_shapes(q, k, v, g, beta, offsets):
@@ -383,33 +400,33 @@ def _delta_shapes(q, k, v, g, beta, offsets):
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must have shape [B, T, heads, N]")
     B, T, Hk, N = q.shape
-    H, dt = v.shape[2], q.dtype
+    H, dt, dev = v.shape[2], q.dtype, q.device
     if dt not in (torch.float32, torch.bfloat16):
         raise TypeError("q must be float32 or bfloat16")
-    _cuda(k, "k", dt, (B, T, Hk, N))
-    _cuda(v, "v", dt, (B, T, H, N))
-    _cuda(g, "g", dt, (B, T, H))
-    _cuda(beta, "beta", dt, (B, T, H))
+    _tensor(k, "k", dt, q.shape, dev)
+    _tensor(v, "v", dt, (B, T, H, N), dev)
+    _tensor(g, "g", dt, (B, T, H), dev)
+    _tensor(beta, "beta", dt, (B, T, H), dev)
     nseq = B
     if offsets is not None:
-        _cuda(offsets, "offsets", torch.int32)
+        _tensor(offsets, "offsets", torch.int32, None, dev)
         if offsets.dim() != 1 or offsets.numel() < 1:
             raise ValueError("offsets must have shape [sequences + 1]")
         nseq = offsets.numel() - 1
-    _same_device(q, k=k, v=v, g=g, beta=beta, offsets=offsets)
     return B, T, Hk, H, N, nseq, dt
 
 
-def _delta_workspace(fn, B, T, Hk, H, N, nseq, packed, bf16):
+@functools.lru_cache(maxsize=1024)
+def _delta_workspace(name, B, T, Hk, H, N, nseq, packed, bf16):
     out = ctypes.c_size_t(0)
-    _check(fn(B, T, Hk, H, N, nseq, packed, bf16, ctypes.byref(out)))
+    _check(getattr(load(), name)(B, T, Hk, H, N, nseq, packed, bf16, ctypes.byref(out)))
     return out.value
 
 
 def delta_forward_workspace_bytes(B, T, Hk, H, N=64, nseq=None, packed=False, bf16=True) -> int:
     """Device scratch (bytes) that a delta-rule forward call of this shape needs."""
-    return _delta_workspace(load().rwkv_delta_forward_workspace_bytes, B, T, Hk, H, N, B if nseq is None else nseq,
-                            packed, bf16)
+    return _delta_workspace("rwkv_delta_forward_workspace_bytes", B, T, Hk, H, N, B if nseq is None else nseq, packed,
+                            bf16)
 
 
 def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=None, want_state=True, o=None, sT=None,
@@ -424,39 +441,41 @@ def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=Non
     """
     lib = load()
     B, T, Hk, H, N, nseq, dt = _delta_shapes(q, k, v, g, beta, offsets)
+    dev = q.device
     if slots is not None:
-        _cuda(slots, "slots", torch.int32, (nseq,))
+        _tensor(slots, "slots", torch.int32, (nseq,), dev)
         if sT is None and want_state:
             if s0 is None:
                 raise ValueError("slots need a pool: s0, sT or both")
             sT = s0
     pool = s0 if s0 is not None else sT
     nslots = nseq if slots is None or pool is None else pool.shape[0]
-    _cuda(s0, "s0", torch.float32, (nslots, H, N, N))
+    state = (nslots, H, N, N)
+    _tensor(s0, "s0", torch.float32, state, dev)
     if o is None:
         o = torch.empty_like(v)
-    _cuda(o, "o", dt, (B, T, H, N))
+    else:
+        _tensor(o, "o", dt, v.shape, dev)
     if sT is None and want_state:
-        sT = torch.empty(nseq, H, N, N, device=q.device, dtype=torch.float32)
-    _cuda(sT, "sT", torch.float32, (nslots, H, N, N))
+        sT = torch.empty(state, device=dev, dtype=torch.float32)
+    elif sT is not s0:
+        _tensor(sT, "sT", torch.float32, state, dev)
     bf = dt == torch.bfloat16
     if workspace is None:
-        need = _delta_workspace(lib.rwkv_delta_forward_workspace_bytes, B, T, Hk, H, N, nseq, offsets is not None, bf)
+        need = _delta_workspace("rwkv_delta_forward_workspace_bytes", B, T, Hk, H, N, nseq, offsets is not None, bf)
         if need:
-            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-    _cuda(workspace, "workspace", torch.uint8)
-    _same_device(q, s0=s0, slots=slots, o=o, sT=sT, workspace=workspace)
-    fn = lib.rwkv_delta_forward_bf16 if bf else lib.rwkv_delta_forward
-    with _on_device_of(lib, q):
-        _check(fn(B, T, Hk, H, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                  N ** -0.5 if scale is None else float(scale), nseq, _ptr(offsets), nslots, _ptr(slots), _ptr(s0),
-                  _ptr(o), _ptr(sT), _ptr(workspace), 0 if workspace is None else workspace.numel()))
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    _tensor(workspace, "workspace", torch.uint8, None, dev)
+    _call(lib, dev, lib.rwkv_delta_forward_bf16 if bf else lib.rwkv_delta_forward, B, T, Hk, H, N, q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else float(scale), nseq,
+          _at(offsets), nslots, _at(slots), _at(s0), o.data_ptr(), _at(sT), _at(workspace),
+          0 if workspace is None else workspace.numel())
     return (o, sT) if want_state else o
 
 
 def delta_backward_workspace_bytes(B, T, Hk, H, N=64, nseq=None, packed=False, bf16=True) -> int:
     """Device scratch (bytes) that a delta-rule backward call of this shape needs."""
-    return _delta_workspace(load().rwkv_delta_backward_workspace_bytes, B, T, Hk, H, N, B if nseq is None else nseq,
+    return _delta_workspace("rwkv_delta_backward_workspace_bytes", B, T, Hk, H, N, B if nseq is None else nseq,
                             packed, bf16)
 
 
@@ -470,25 +489,23 @@ def delta_backward(q, k, v, g, beta, do, scale=None, s0=None, dsT=None, offsets=
     """
     lib = load()
     B, T, Hk, H, N, nseq, dt = _delta_shapes(q, k, v, g, beta, offsets)
-    _cuda(do, "do", dt, (B, T, H, N))
-    _cuda(s0, "s0", torch.float32, (nseq, H, N, N))
-    _cuda(dsT, "dsT", torch.float32, (nseq, H, N, N))
+    dev, state = q.device, (nseq, H, N, N)
+    _tensor(do, "do", dt, v.shape, dev)
+    _tensor(s0, "s0", torch.float32, state, dev)
+    _tensor(dsT, "dsT", torch.float32, state, dev)
     make = torch.empty_like if offsets is None else torch.zeros_like
     out = {"dq": make(q), "dk": make(k), "dv": make(v), "dg": make(g), "dbeta": make(beta)}
-    out["ds0"] = torch.empty(nseq, H, N, N, device=q.device, dtype=torch.float32) if want_ds0 else None
+    if want_ds0:
+        out["ds0"] = torch.empty(state, device=dev, dtype=torch.float32)
+    bf = dt == torch.bfloat16
     if workspace is None:
-        need = delta_backward_workspace_bytes(B, T, Hk, H, N, nseq, offsets is not None, dt == torch.bfloat16)
-        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
-    _cuda(workspace, "workspace", torch.uint8)
-    _same_device(q, do=do, s0=s0, dsT=dsT, workspace=workspace)
-    fn = lib.rwkv_delta_backward_bf16 if dt == torch.bfloat16 else lib.rwkv_delta_backward
-    with _on_device_of(lib, q):
-        _check(fn(B, T, Hk, H, N, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                  N ** -0.5 if scale is None else float(scale), nseq, _ptr(offsets), _ptr(s0), _ptr(do), _ptr(dsT),
-                  _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
-                  _ptr(out["ds0"]), _ptr(workspace), ctypes.c_size_t(workspace.numel())))
-    if not want_ds0:
-        del out["ds0"]
+        need = _delta_workspace("rwkv_delta_backward_workspace_bytes", B, T, Hk, H, N, nseq, offsets is not None, bf)
+        workspace = torch.empty(max(need, 16), device=dev, dtype=torch.uint8)
+    _tensor(workspace, "workspace", torch.uint8, None, dev)
+    _call(lib, dev, lib.rwkv_delta_backward_bf16 if bf else lib.rwkv_delta_backward, B, T, Hk, H, N, q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N ** -0.5 if scale is None else float(scale), nseq,
+          _at(offsets), _at(s0), do.data_ptr(), _at(dsT), *(out[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")),
+          _at(out.get("ds0")), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -515,11 +532,10 @@ def state_copy(pool, src, dst, slot_dim=0):
     """
     lib = load()
     layers, nslots, slot_bytes = _pool_shape(pool, slot_dim)
-    _cuda(src, "src", torch.int32)
-    _cuda(dst, "dst", torch.int32, src.shape)
-    _same_device(pool, src=src, dst=dst)
-    with _on_device_of(lib, pool):
-        _check(lib.rwkv_state_copy(layers, nslots, slot_bytes, _ptr(pool), src.numel(), _ptr(src), _ptr(dst)))
+    _tensor(src, "src", torch.int32, None, pool.device)
+    _tensor(dst, "dst", torch.int32, src.shape, pool.device)
+    _call(lib, pool.device, lib.rwkv_state_copy, layers, nslots, slot_bytes, pool.data_ptr(), src.numel(), src.data_ptr(),
+          dst.data_ptr())
 
 
 def state_compact(pool, live, slot_dim=0):
@@ -531,14 +547,13 @@ def state_compact(pool, live, slot_dim=0):
     """
     lib = load()
     layers, nslots, slot_bytes = _pool_shape(pool, slot_dim)
-    _cuda(live, "live", None, (nslots,))
-    if live.dtype not in (torch.bool, torch.uint8):
+    if isinstance(live, torch.Tensor) and live.dtype not in (torch.bool, torch.uint8):
         raise TypeError("live must be bool or uint8")
-    _same_device(pool, live=live)
+    _tensor(live, "live", getattr(live, "dtype", None), (nslots,), pool.device)
     new_index = torch.empty(nslots, device=pool.device, dtype=torch.int32)
     count = torch.empty(1, device=pool.device, dtype=torch.int32)
-    with _on_device_of(lib, pool):
-        _check(lib.rwkv_state_compact(layers, nslots, slot_bytes, _ptr(pool), _ptr(live), _ptr(new_index), _ptr(count)))
+    _call(lib, pool.device, lib.rwkv_state_compact, layers, nslots, slot_bytes, pool.data_ptr(), live.data_ptr(),
+          new_index.data_ptr(), count.data_ptr())
     return new_index, count
 
 
