@@ -26,6 +26,8 @@
 // status word, waits (bounded) for its own copies and MMAs, frees its tensor memory and returns.
 #include "delta_tc.cuh"
 
+#include <algorithm>
+
 namespace wkv {
 namespace {
 using namespace dtc;
@@ -458,23 +460,30 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 //   diag(scale gamma) dO S_prev^T + A1 K, dW S_prev^T, (A2 + A2^T) K + A1^T Q, U dS^T -> the gradients
 // A1 and A2 enter the second round rounded to bf16.  For dg, where the terms of A1 and of A2 can
 // cancel (keys near one another), what the rounding left is added back as its row and column sums.
-// Nine tiles: Q, K, dO (then diag(scale gamma) dO in its place), U, S_prev, dW, dS, A1, A2.
+//
+// The blocks stay and take chunks in turn.  Thirteen tiles: Q, K and dW twice (the next chunk's load
+// while this one's are still read), V, dO (then diag(scale gamma) dO in its place), U, S_prev, dS, A1,
+// A2.  The loads of the next chunk start as soon as the second round of products is done.  dQ, dK and
+// dV of a whole chunk leave as tiles (from where A1, A2 and dW were): a row of a thread's own is 16
+// bytes, and stores of those were the kernel's largest use of the shared-memory pipe.
 constexpr int kGThreads = 256;
-constexpr int GO_Q = 0, GO_K = kTile, GO_DO = 2 * kTile, GO_U = 3 * kTile, GO_S = 4 * kTile, GO_DW = 5 * kTile;
-constexpr int GO_DS = 6 * kTile, GO_A1 = 7 * kTile, GO_A2 = 8 * kTile, GO_DEC = 9 * kTile;
+constexpr int GO_Q = 0, GO_K = 2 * kTile, GO_DW = 4 * kTile;  // + kTile * (item % 2)
+constexpr int GO_V = 6 * kTile, GO_DO = 7 * kTile, GO_U = 8 * kTile, GO_S = 9 * kTile, GO_DS = 10 * kTile;
+constexpr int GO_A1 = 11 * kTile, GO_A2 = 12 * kTile, GO_DEC = 13 * kTile;
 constexpr int GO_ARR = GO_DEC + static_cast<int>(sizeof(Decays));
 constexpr int GO_RED = GO_ARR + static_cast<int>(sizeof(ChunkArrays));  // [4 sums][2 halves][64], [8] warps' sums, [4]
 constexpr int GO_COL = GO_RED + 4 * 2 * 256 + 64;   // [4 block rows][64] column sums
 constexpr int GO_DIAG = GO_COL + 4 * 256;           // [64] diagonal of A1
 constexpr int GO_BAR = GO_DIAG + 256;
 constexpr int kGSmemBytes = GO_BAR + 32 + 1024;
+static_assert(2 * (kGSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
 constexpr uint32_t GC_DOU = 0, GC_DWU = 64, GC_QK = 128, GC_KK = 192;           // first round
 constexpr uint32_t GC_DQ = 0, GC_DK = 64, GC_DWS = 128, GC_UDS = 192;           // second
 
 struct GradParams {
     int64_t B, T, Hk, H, nseq;
     const int32_t *offsets;
-    const __nv_bfloat16 *v, *g, *beta;
+    const __nv_bfloat16 *g, *beta;
     float scale;
     const unsigned char *states, *us, *ds, *dw;  // [chunks][H] tiles
     int64_t nchunks;
@@ -559,89 +568,130 @@ __device__ __forceinline__ void st_blocks(float *p, const Row &v)
             make_float4(lo(v.x[2 * i]), hi(v.x[2 * i]), lo(v.x[2 * i + 1]), hi(v.x[2 * i + 1]));
 }
 
+// One (chunk, value head).
+struct Item {
+    int64_t h, hk, t0;
+    int tv;          // tokens of the chunk, 0: there is no such chunk
+    int row_b, row_t;  // tensor-map coordinates of the first token
+};
+__device__ __forceinline__ Item item_at(const GradParams &p, uint32_t n)
+{
+    const uint32_t heads = static_cast<uint32_t>(p.H), id = n / heads, h = n % heads;
+    int64_t seq, first, len;
+    const int c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
+    Item x;
+    x.h = h;
+    x.hk = h / (heads / static_cast<uint32_t>(p.Hk));
+    x.t0 = first + static_cast<int64_t>(c) * kC;
+    const int64_t left = len - (x.t0 - first);
+    x.tv = c < 0 ? 0 : static_cast<int>(left < kC ? left : kC);
+    x.row_b = p.offsets ? 0 : static_cast<int>(seq);
+    x.row_t = static_cast<int>(p.offsets ? x.t0 : x.t0 - first);
+    return x;
+}
+
 __global__ void __launch_bounds__(kGThreads, 2)
 delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                      const __grid_constant__ CUtensorMap map_do, const GradParams p)
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                      const __grid_constant__ CUtensorMap map_dq, const __grid_constant__ CUtensorMap map_dk,
+                      const __grid_constant__ CUtensorMap map_dv, const GradParams p)
 {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const uint32_t heads = static_cast<uint32_t>(p.H), id = blockIdx.x / heads;
-    const int64_t h = blockIdx.x % heads, hk = static_cast<uint32_t>(h) / (heads / static_cast<uint32_t>(p.Hk));
-    int64_t seq, first, len;
-    const int c = chunk_of(p.offsets, p.nseq, p.T, id, &seq, &first, &len);
-    if (c < 0) return;  // a number that no chunk has
-    const int64_t t0 = first + static_cast<int64_t>(c) * kC, ntok = p.B * p.T;
-    const int tv = static_cast<int>(len - (t0 - first) < kC ? len - (t0 - first) : kC);
-    const uint32_t bar0 = smem_u32(sm + GO_BAR), bar1 = bar0 + 8, bar2 = bar0 + 16;
+    const int64_t ntok = p.B * p.T;
+    const uint32_t total = static_cast<uint32_t>(p.nchunks * p.H);
+    const uint32_t bar0 = smem_u32(sm + GO_BAR), bar1 = bar0 + 8, bar2 = bar0 + 16;  // tiles there; rounds done
     volatile uint32_t *tm = reinterpret_cast<volatile uint32_t *>(sm + GO_BAR + 24);
     Decays &dec = *reinterpret_cast<Decays *>(sm + GO_DEC);
     ChunkArrays &arr = *reinterpret_cast<ChunkArrays *>(sm + GO_ARR);
     float *red = reinterpret_cast<float *>(sm + GO_RED), *diag = reinterpret_cast<float *>(sm + GO_DIAG);
     float *cols = reinterpret_cast<float *>(sm + GO_COL);
 
+    // the block's next item that is a chunk (total: none left)
+    auto next_item = [&](uint32_t n, Item *x) -> uint32_t {
+        for (; n < total; n += gridDim.x) {
+            *x = item_at(p, n);
+            if (x->tv > 0) break;
+        }
+        return n < total ? n : total;
+    };
+    auto load = [&](uint32_t n, const Item &x, int buf) {  // one thread
+        const uint32_t id = n / static_cast<uint32_t>(p.H);
+        const int64_t tile = static_cast<int64_t>(n) * kTile;  // n = id * H + h
+        if (!tma_coord_ok(p.status, 0, 2, kN, x.row_t, p.T) || !in_bounds(p.status, id, 1, p.nchunks)) return;
+        const int h = static_cast<int>(x.h), hk = static_cast<int>(x.hk);
+        bar_expect_tx(bar0, 8 * kTile);
+        bulk_load(smem_u32(sm + GO_U), p.us + tile, kTile, bar0);
+        bulk_load(smem_u32(sm + GO_DW + kTile * buf), p.dw + tile, kTile, bar0);
+        tma_load_4d(smem_u32(sm + GO_DO), &map_do, 0, h, x.row_t, x.row_b, bar0);
+        tma_load_4d(smem_u32(sm + GO_Q + kTile * buf), &map_q, 0, hk, x.row_t, x.row_b, bar0);
+        tma_load_4d(smem_u32(sm + GO_K + kTile * buf), &map_k, 0, hk, x.row_t, x.row_b, bar0);
+        tma_load_4d(smem_u32(sm + GO_V), &map_v, 0, h, x.row_t, x.row_b, bar0);
+        bulk_load(smem_u32(sm + GO_S), p.states + tile, kTile, bar0);
+        bulk_load(smem_u32(sm + GO_DS), p.ds + tile, kTile, bar0);
+    };
+    const int st = tid - 32;  // warps 1 and 2: the token whose decay this thread prepares
+    uint16_t g_next = 0, b_next = 0;
+    auto fetch = [&](const Item &x) {
+        g_next = b_next = 0;
+        if (st < 0 || st >= 64 || st >= x.tv || !in_bounds(p.status, x.t0 + st, 1, ntok)) return;
+        const int64_t at = (x.t0 + st) * p.H + x.h;
+        g_next = reinterpret_cast<const uint16_t *>(p.g)[at];
+        b_next = reinterpret_cast<const uint16_t *>(p.beta)[at];
+    };
+    Item cur, nxt;
+    uint32_t n = next_item(blockIdx.x, &cur);
+    if (n >= total) return;
     if (warp == 0) {
         if (lane == 0) {
             for (int i = 0; i < 3; ++i) bar_init(bar0 + 8 * i, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            const int row_b = p.offsets ? 0 : static_cast<int>(seq), row_t = static_cast<int>(p.offsets ? t0 : t0 - first);
-            const int64_t tile = (static_cast<int64_t>(id) * p.H + h) * kTile;
-            if (tma_coord_ok(p.status, 0, 2, kN, row_t, p.T) && in_bounds(p.status, id, 1, p.nchunks)) {
-                bar_expect_tx(bar0, 7 * kTile);
-                tma_load_4d(smem_u32(sm + GO_Q), &map_q, 0, static_cast<int>(hk), row_t, row_b, bar0);
-                tma_load_4d(smem_u32(sm + GO_K), &map_k, 0, static_cast<int>(hk), row_t, row_b, bar0);
-                tma_load_4d(smem_u32(sm + GO_DO), &map_do, 0, static_cast<int>(h), row_t, row_b, bar0);
-                bulk_load(smem_u32(sm + GO_U), p.us + tile, kTile, bar0);
-                bulk_load(smem_u32(sm + GO_S), p.states + tile, kTile, bar0);
-                bulk_load(smem_u32(sm + GO_DW), p.dw + tile, kTile, bar0);
-                bulk_load(smem_u32(sm + GO_DS), p.ds + tile, kTile, bar0);
-            }
+            load(n, cur, 0);
         }
         __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(const_cast<uint32_t *>(tm))),
                      "r"(256u));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    } else if (warp < 3) {
-        const int t = tid - 32;
-        float g = 0.f, b = 0.f;
-        if (t < tv && in_bounds(p.status, t0 + t, 1, ntok)) {
-            g = __bfloat162float(p.g[(t0 + t) * p.H + h]);
-            b = __bfloat162float(p.beta[(t0 + t) * p.H + h]);
-        }
-        scan_decays<1>(dec, arr, t, g, b);
     }
-    // this thread's row and the first of its columns; v of that place comes straight from memory
+    fetch(cur);
+    fence_before();
+    __syncthreads();
+    fence_after();
     const int q = warp & 3, half = warp >> 2, row = 16 * q + (lane & 15), col = 32 * half + 8 * (lane >> 4);
-    const int64_t token = t0 + row, at = (token * p.H + h) * kN + col;
-    const bool valid = row < tv && in_bounds(p.status, token, 1, ntok);
-    const uint32_t sw[2] = {swz(row, 2 * col), swz(row, 2 * col + 32)};  // its place in a tile
-    uint4 vv[2] = {};
-    if (valid) {
-        vv[0] = *reinterpret_cast<const uint4 *>(p.v + at);
-        vv[1] = *reinterpret_cast<const uint4 *>(p.v + at + 16);
-    }
+    const uint32_t sw[2] = {swz(row, 2 * col), swz(row, 2 * col + 32)};  // this thread's places in a tile
+    const uint32_t tbase = tm[0], tl = tbase + (static_cast<uint32_t>(32 * q) << 16) + 32 * half;
     auto tile_row = [&](int tile, Row &x) {
         const uint4 y[2] = {*reinterpret_cast<const uint4 *>(sm + tile + sw[0]), *reinterpret_cast<const uint4 *>(sm + tile + sw[1])};
         unpack_row(y, x);
     };
-    fence_before();
-    __syncthreads();
-    fence_after();
-    const uint32_t tbase = tm[0], tl = tbase + (static_cast<uint32_t>(32 * q) << 16) + 32 * half;
-    int ok = bar_wait(bar0, 0, p.spin_limit);
-    if (tv < kC) {
-        zero_rows(sm + GO_Q, tv, tid, kGThreads);
-        zero_rows(sm + GO_K, tv, tid, kGThreads);
-        zero_rows(sm + GO_DO, tv, tid, kGThreads);
-        fence_async_smem();
-    }
-    const bool go = !__syncthreads_or(!ok);
-    if (go) {
-        const uint32_t aQ = smem_u32(sm + GO_Q), aK = smem_u32(sm + GO_K), aO = smem_u32(sm + GO_DO);
-        const uint32_t aU = smem_u32(sm + GO_U), aS = smem_u32(sm + GO_S), aW = smem_u32(sm + GO_DW);
-        const uint32_t aD = smem_u32(sm + GO_DS), a1 = smem_u32(sm + GO_A1);
+    auto put_row = [&](int tile, const Row &x) {
+        *reinterpret_cast<uint4 *>(sm + tile + sw[0]) = pack_block(x, 0);
+        *reinterpret_cast<uint4 *>(sm + tile + sw[1]) = pack_block(x, 1);
+    };
+
+    int ok = 1;
+    for (int it = 0; n < total; ++it, cur = nxt) {
+        const int buf = it & 1, ph = it & 1, tQ = GO_Q + kTile * buf, tK = GO_K + kTile * buf, tW = GO_DW + kTile * buf;
+        const uint32_t aQ = smem_u32(sm + tQ), aK = smem_u32(sm + tK), aW = smem_u32(sm + tW), aO = smem_u32(sm + GO_DO);
+        const uint32_t aU = smem_u32(sm + GO_U), aS = smem_u32(sm + GO_S), aD = smem_u32(sm + GO_DS);
+        const uint32_t a1 = smem_u32(sm + GO_A1), a2 = smem_u32(sm + GO_A2);
+        const int64_t token = cur.t0 + row, at = (token * p.H + cur.h) * kN + col;
+        const bool whole = cur.tv == kC, valid = row < cur.tv && in_bounds(p.status, token, 1, ntok);
+        ok = bar_wait(bar0, ph, p.spin_limit);
+        if (!whole) {
+            zero_rows(sm + tQ, cur.tv, tid, kGThreads);
+            zero_rows(sm + tK, cur.tv, tid, kGThreads);
+            zero_rows(sm + GO_V, cur.tv, tid, kGThreads);
+            zero_rows(sm + GO_DO, cur.tv, tid, kGThreads);
+            fence_async_smem();
+        }
+        if (__syncthreads_or(!ok)) {
+            ok = 0;
+            break;
+        }
         if (warp == 0) {
             const uint64_t dO = desc_k(aO), dU = desc_k(aU), dW = desc_k(aW), dK = desc_k(aK), dQ = desc_k(aQ);
             if (elect_one()) {
@@ -652,23 +702,25 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 mma_commit(bar1);
             }
             __syncwarp();
+        } else if (warp < 3) {
+            scan_decays<1>(dec, arr, st, widen(g_next), widen(b_next));
         }
-        const float beta = arr.beta[row], gam = arr.gamma[row], tail = arr.tail[row];
-        // ---- dV and the row's dW.V; <dS, S_prev>; decays of the blocks left of the diagonal
+        const uint32_t n2 = next_item(n + gridDim.x, &nxt);
+        if (n2 < total) fetch(nxt);
+        // ---- the row's dW.V; <dS, S_prev>
         float dots, dwv;
         {
             Row x, y;
-            tile_row(GO_DW, x);
-            unpack_row(vv, y);
+            tile_row(tW, x);
+            tile_row(GO_V, y);
             dwv = dot(x, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x.x[i] = mul2(x.x[i], pk(beta, beta));
-            if (valid) st_blocks(p.dv + at, x);
             tile_row(GO_S, x);
             tile_row(GO_DS, y);
             dots = dot(x, y);
         }
-        Row gm;  // Gamma, zero right of the diagonal; 1 on it
+        __syncthreads();
+        const float beta = arr.beta[row], gam = arr.gamma[row], tail = arr.tail[row];
+        Row gm;  // Gamma, 1 on the diagonal
         const float n0 = dec.pn[row], f0 = dec.pf[row];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -681,7 +733,7 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 const float rf = ex2_approx((n0 + mn) + (f0 + mf));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) gm.x[4 * b + i] = mul2(ld_p2(dec.cf + col + 16 * b + 2 * i), pk(rf, rf));
-            } else {
+            } else if (blk == q) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int cc = col + 16 * b + 2 * i;
@@ -691,8 +743,16 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
             }
         }
-        ok = bar_wait(bar1, 0, p.spin_limit);
-        fence_after();
+        {
+            Row x;  // the first round's reading of dO is over once its results are there: see below
+            ok = bar_wait(bar1, ph, p.spin_limit);
+            fence_after();
+            const float sg = p.scale * gam;
+            tile_row(GO_DO, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x.x[i] = mul2(x.x[i], pk(sg, sg));
+            put_row(GO_DO, x);
+        }
         // ---- A1, A2, sum Gamma (k k) (dW.U), and what rounding A1 and A2 leaves
         float xt = 0.f, rowd = 0.f;
         {
@@ -712,23 +772,23 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int k = 4 * b + i, cc = col + 16 * b + 2 * i;
-                        P2 a1 = mul2(mul2(gm.x[k], pk(p.scale, p.scale)), o.x[k]), g = gm.x[k];
+                        P2 v1 = mul2(mul2(gm.x[k], pk(p.scale, p.scale)), o.x[k]), g = gm.x[k];
                         if (blk == q) {  // A1's diagonal is added to dQ and dK at the end
-                            if (cc == row) diag[row] = lo(a1);
-                            if (cc + 1 == row) diag[row] = hi(a1);
-                            a1 = pk(cc < row ? lo(a1) : 0.f, cc + 1 < row ? hi(a1) : 0.f);
+                            if (cc == row) diag[row] = lo(v1);
+                            if (cc + 1 == row) diag[row] = hi(v1);
+                            v1 = pk(cc < row ? lo(v1) : 0.f, cc + 1 < row ? hi(v1) : 0.f);
                             g = pk(cc < row ? lo(g) : 0.f, cc + 1 < row ? hi(g) : 0.f);
                         }
                         const P2 gw = mul2(g, wu.x[k]);
                         xs = fma2(gw, kk.x[k], xs);
-                        const P2 a2 = mul2(gw, pk(-beta, -beta));
-                        h1[i] = pack2(a1);
-                        h2[i] = pack2(a2);
+                        const P2 v2 = mul2(gw, pk(-beta, -beta));
+                        h1[i] = pack2(v1);
+                        h2[i] = pack2(v2);
                         // x, taken twice, has A2's row sum unrounded already: its remainder counts the
                         // other way there
                         const P2 m1 = pk(-1.f, -1.f);
-                        const P2 d1 = mul2(fma2(unpack2(h1[i]), m1, a1), qk.x[k]);
-                        const P2 d2 = mul2(fma2(unpack2(h2[i]), m1, a2), kk.x[k]);
+                        const P2 d1 = mul2(fma2(unpack2(h1[i]), m1, v1), qk.x[k]);
+                        const P2 d2 = mul2(fma2(unpack2(h2[i]), m1, v2), kk.x[k]);
                         left[i] = add2(d1, d2);
                         rows = add2(rows, fma2(d2, m1, d1));
                     }
@@ -741,21 +801,14 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 *reinterpret_cast<uint4 *>(sm + GO_A2 + sw[b]) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
             }
         }
-        {
-            Row x;
-            const float sg = p.scale * gam;
-            tile_row(GO_DO, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x.x[i] = mul2(x.x[i], pk(sg, sg));
-            *reinterpret_cast<uint4 *>(sm + GO_DO + sw[0]) = pack_block(x, 0);
-            *reinterpret_cast<uint4 *>(sm + GO_DO + sw[1]) = pack_block(x, 1);
-        }
         fence_async_smem();
         fence_before();
-        ok = !__syncthreads_or(!ok);
+        if (__syncthreads_or(!ok)) {
+            ok = 0;
+            break;
+        }
         fence_after();
-        if (warp == 0 && ok) {
-            const uint32_t a2 = smem_u32(sm + GO_A2);
+        if (warp == 0) {
             const uint64_t dO = desc_k(aO), dS = desc_k(aS), dA1 = desc_k(a1), dA1t = desc_mn(a1), dA2 = desc_k(a2), dA2t = desc_mn(a2);
             const uint64_t dKn = desc_mn(aK), dQn = desc_mn(aQ), dU = desc_k(aU), dD = desc_k(aD), dW = desc_k(aW);
             if (elect_one()) {
@@ -770,25 +823,34 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             }
             __syncwarp();
         }
-        float e = 0.f, r2 = 0.f;
-        if (ok) ok = bar_wait(bar2, 0, p.spin_limit);
+        Row qr, kr;
+        tile_row(tQ, qr);
+        tile_row(tK, kr);
+        ok = bar_wait(bar2, ph, p.spin_limit);
         fence_after();
+        if (n2 < total && warp == 7 && elect_one()) {  // the tiles are free (this thread stored the last chunk's)
+            bulk_wait_read<0>();
+            load(n2, nxt, buf ^ 1);
+        }
+        __syncwarp();
+        // ---- dQ, dK, dV
+        float e, r2;
         {
             const float a = diag[row], bg = -beta * gam;
-            const P2 a2 = pk(a, a);
-            Row qr, kr;
+            const P2 aa = pk(a, a);
             Raw rx, ry, rz;
             tmem_ld_blocks(tl + GC_DQ, rx);
-            tile_row(GO_Q, qr);
-            tile_row(GO_K, kr);
             tmem_wait_ld();
             Row x = row_of(rx);
             e = dot(x, qr) + rowd;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x.x[i] = fma2(a2, kr.x[i], x.x[i]);
-            if (valid) {
-                if (p.dq_h) st_blocks(p.dq_h + at, x);
-                else st_blocks(p.dq + at, x);
+            for (int i = 0; i < 8; ++i) x.x[i] = fma2(aa, kr.x[i], x.x[i]);
+            if (p.dq_h) {
+                if (valid) st_blocks(p.dq_h + at, x);
+            } else if (whole) {
+                put_row(GO_A1, x);
+            } else if (valid) {
+                st_blocks(p.dq + at, x);
             }
             tmem_ld_blocks(tl + GC_DK, rx);
             tmem_ld_blocks(tl + GC_DWS, ry);
@@ -806,12 +868,21 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             e -= dot(kr, x);
             r2 = dot(kr, z);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x.x[i] = add2(x.x[i], fma2(a2, qr.x[i], z.x[i]));
-            if (valid) {
-                if (p.dk_h) st_blocks(p.dk_h + at, x);
-                else st_blocks(p.dk + at, x);
+            for (int i = 0; i < 8; ++i) x.x[i] = add2(x.x[i], fma2(aa, qr.x[i], z.x[i]));
+            if (p.dk_h) {
+                if (valid) st_blocks(p.dk_h + at, x);
+            } else if (whole) {
+                put_row(GO_A2, x);
+            } else if (valid) {
+                st_blocks(p.dk + at, x);
             }
+            tile_row(tW, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x.x[i] = mul2(x.x[i], pk(beta, beta));
+            if (whole) put_row(tW, x);
+            else if (valid) st_blocks(p.dv + at, x);
         }
+        fence_async_smem();
         // ---- sums over a row's four threads, and over the chunk
         dwv += __shfl_xor_sync(0xffffffffu, dwv, 16);
         xt += __shfl_xor_sync(0xffffffffu, xt, 16);
@@ -826,8 +897,27 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             red[384 + half * 64 + row] = r2;
         }
         if (lane == 0) red[512 + warp] = dots;
-        __syncthreads();
-        if (warp < 2) {
+        fence_before();
+        if (__syncthreads_or(!ok)) {
+            ok = 0;
+            break;
+        }
+        fence_after();
+        if (warp == 7) {
+            if (elect_one()) {
+                if (whole && tma_coord_ok(p.status, 0, 2, kN, cur.row_t + kC - 1, p.T)) {
+                    const int h = static_cast<int>(cur.h), hk = static_cast<int>(cur.hk);
+                    if (!p.dq_h) {
+                        tma_store_4d(&map_dq, 0, hk, cur.row_t, cur.row_b, a1);
+                        tma_store_4d(&map_dk, 0, hk, cur.row_t, cur.row_b, a2);
+                    }
+                    tma_store_4d(&map_dv, 0, h, cur.row_t, cur.row_b, aW);
+                }
+                bulk_commit();
+                bulk_wait_read<0>();  // A1 and A2 are written again before this thread's next wait
+            }
+            __syncwarp();
+        } else if (warp < 2) {
             const int t = tid;
             const float x = red[128 + t] + red[192 + t], own = red[384 + t] + red[448 + t];
             float s = red[256 + t] + red[320 + t] - 2.f * arr.beta[t] * x, before = own;
@@ -842,24 +932,27 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             if (lane == 31) red[522 + warp] = before;
             before = __shfl_up_sync(0xffffffffu, before, 1);  // without the token itself
             if (lane == 0) before = 0.f;
-            group_sync<1, 64>();
+            group_sync<2, 64>();
             if (warp == 0) s += red[521];
             else before += red[522];
-            float dot = 0.f;
+            float dot_all = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) dot += red[512 + w];
-            if (t < tv && in_bounds(p.status, t0 + t, 1, ntok)) {
-                p.dg[(t0 + t) * p.H + h] = __float2bfloat16_rn(s + (before + arr.gamma[kC - 1] * dot));
-                p.dbeta[(t0 + t) * p.H + h] = __float2bfloat16_rn(red[t] + red[64 + t] - x);
+            for (int w = 0; w < 8; ++w) dot_all += red[512 + w];
+            if (t < cur.tv && in_bounds(p.status, cur.t0 + t, 1, ntok)) {
+                p.dg[(cur.t0 + t) * p.H + cur.h] = __float2bfloat16_rn(s + (before + arr.gamma[kC - 1] * dot_all));
+                p.dbeta[(cur.t0 + t) * p.H + cur.h] = __float2bfloat16_rn(red[t] + red[64 + t] - x);
             }
         }
+        n = n2;
     }
+    if (warp == 7 && elect_one()) bulk_wait_all();
     fence_before();
-    const int bad = __syncthreads_or(!go || !ok);
+    const int bad = __syncthreads_or(!ok);
     fence_after();
     if (bad && tid == 0) {
         record_status(p.status, kStatusTimeout);
-        for (int i = 0; i < 3; ++i) bar_wait(bar0 + 8 * i, 0, 200);  // what is in flight
+        for (int i = 0; i < 3; ++i)  // what is in flight
+            for (uint32_t ph = 0; ph < 2; ++ph) bar_wait(bar0 + 8 * i, ph, 200);
     }
     __syncthreads();
     if (warp == 0)
@@ -897,8 +990,10 @@ cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s)
     if (chunks * f.H > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const Layout l = layout(f);
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
-    CUtensorMap mq, mk, mo;
-    if (!make_map(&mq, f.q, f.B, f.T, f.Hk) || !make_map(&mk, f.k, f.B, f.T, f.Hk) || !make_map(&mo, a.dout, f.B, f.T, f.H))
+    CUtensorMap mq, mk, mv, mo, mdq, mdk, mdv;
+    if (!make_map(&mq, f.q, f.B, f.T, f.Hk) || !make_map(&mk, f.k, f.B, f.T, f.Hk) || !make_map(&mv, f.v, f.B, f.T, f.H) ||
+        !make_map(&mo, a.dout, f.B, f.T, f.H) || !make_map(&mdq, a.dq, f.B, f.T, f.Hk) ||
+        !make_map(&mdk, a.dk, f.B, f.T, f.Hk) || !make_map(&mdv, a.dv, f.B, f.T, f.H))
         return cudaErrorInvalidValue;
     cudaError_t e = delta_prep_launch(f, ws + l.t, s);
     if (e != cudaSuccess) return e;
@@ -918,12 +1013,17 @@ cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s)
     const bool shared = f.H != f.Hk;
     float *dq_h = shared ? reinterpret_cast<float *>(ws + l.shares) : nullptr;
     float *dk_h = shared ? dq_h + f.B * f.T * f.H * kN : nullptr;
-    const GradParams gp{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, static_cast<const __nv_bfloat16 *>(f.v), g, beta, f.scale,
+    const GradParams gp{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, g, beta, f.scale,
                         ws + l.states, ws + l.us, ws + l.ds, ws + l.dw, chunks,
                         static_cast<__nv_bfloat16 *>(a.dq), static_cast<__nv_bfloat16 *>(a.dk),
                         static_cast<__nv_bfloat16 *>(a.dv), static_cast<__nv_bfloat16 *>(a.dg),
                         static_cast<__nv_bfloat16 *>(a.dbeta), dq_h, dk_h, f.status, 100000u};
-    delta_bwd_grad_kernel<<<static_cast<unsigned>(chunks * f.H), kGThreads, kGSmemBytes, s>>>(mq, mk, mo, gp);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        sms <= 0)
+        sms = 148;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(chunks * f.H, 2LL * sms));
+    delta_bwd_grad_kernel<<<grid, kGThreads, kGSmemBytes, s>>>(mq, mk, mv, mo, mdq, mdk, mdv, gp);
     e = cudaGetLastError();
     if (e == cudaSuccess && shared) e = delta_sum_heads_launch(a, dq_h, dk_h, s);
     return e;
