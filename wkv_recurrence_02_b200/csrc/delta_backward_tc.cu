@@ -211,11 +211,8 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             uint32_t ph[4][4], pl[4][4];
             form_p<true>(dec, w, lane, qk, p.scale, ph, pl);
             fence_before();
-            if (named_sync_or(1, 128, !ok || misc[1])) {
-                abort = 1;
-                misc[1] = 1;
-                break;
-            }
+            if (misc[1]) ok = 0;
+            group_sync<1, 128>();
             if (w >= 2 && n + 1 < nchunks) scan(n + 1);
             // ---- P^T dO; the pair of tiles was last read by the product that bar_y stands for
             if (ok && n > 0) ok = bar_wait(bar_y, (n - 1) & 1, spin);
@@ -270,6 +267,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 __syncwarp();
                 if (n + 1 < nchunks && !products(n + 1)) ok = 0;
             }
+            if (!ok) misc[1] = 1;
         }
     } else {
         // ------------------------------------------------------------------ chain group
@@ -315,20 +313,16 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         for (int n = 0; n < nchunks; ++n) {
             const uint32_t aK = smem_u32(sm + OFF_K + kTile * (n & 1));
             const int64_t id = chunk0 + nchunks - 1 - n, tile = (id * p.H + h) * kTile;
-            // ---- dS hi, lo; K dS.  Whether to stop is voted on here
+            // ---- dS hi, lo; K dS
+            if (misc[1]) ok = 0;
             store_split(S, 0, tA, tB);
             store_split(S + 8, 1, tA, tB);
-            if (ok) ok = bar_wait(bar_s0 + 8 * (n % 3), (n / 3) & 1, spin);
-            if (ok) ok = bar_wait(bar_k0 + 8 * (n & 1), (n >> 1) & 1, spin);
-            fence_async_smem();
-            fence_before();
-            if (named_sync_or(2, 128, !ok || misc[1])) {
-                abort = 1;
-                break;
-            }
-            fence_after();
+            if (n == 0 && ok) ok = bar_wait(bar_s0, 0, spin);  // tail rows are zeroed
+            meet();
             if (warp == 4) {
                 const uint64_t dK = desc_k(aK);
+                if (ok) ok = bar_wait_spin(bar_k0 + 8 * (n & 1), (n >> 1) & 1, spin * 64u);
+                __syncwarp();
                 if (elect_one()) {
                     mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, idesc(128, 0, 1));
                     mma_commit(bar_x);
@@ -339,10 +333,11 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 bulk_wait_read<0>();
                 bar_arrive(bar_as);
             } else if (warp == 7 && n > 0 && n + 1 < nchunks) {  // dS is there: the chunk before is done with its tiles
-                if (elect_one()) load_tiles(n + 1);
+                if (elect_one() && ok) load_tiles(n + 1);
             }
             __syncwarp();
             // ---- dU = P^T dO + diag(tail) K dS
+            if (ok) ok = bar_wait(bar_s0 + 8 * (n % 3), (n / 3) & 1, spin);
             const ChunkArrays &arr = reinterpret_cast<const ChunkArrays *>(sm + OFF_ARR)[n % 3];
             const float bg = -arr.beta[row] * arr.gamma[row], tail = arr.tail[row], gC = arr.gamma[kC - 1];
             if (ok) ok = bar_wait(bar_d0, n & 1, spin);
@@ -403,7 +398,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 bulk_wait_read<0>();
                 bar_arrive(bar_cs);
             } else if (warp == 7 && n + 1 < nchunks) {
-                if (elect_one()) load_t(n + 1);  // dW is there: T has been read
+                if (elect_one() && ok) load_t(n + 1);  // dW is there: T has been read
             }
             __syncwarp();
             // ---- dS
@@ -420,6 +415,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             }
             fence_before();
             bar_arrive(bar_yr);
+            if (!ok) misc[1] = 1;  // and its waits pass from here on, in this thread and soon in all
         }
         if (warp == 5 && lane == 0) bulk_wait_all();
         if (abort) ok = 0;

@@ -221,13 +221,11 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
         }
         for (int c = 0; c < nchunks && !abort; ++c) {
-            if (named_sync_or(1, 128, !ok || misc[1])) {  // Q K^T and the decays have been read
-                abort = 1;
-                misc[1] = 1;
-                break;
-            }
+            if (misc[1]) ok = 0;
+            group_sync<1, 128>();  // Q K^T and the decays have been read
             if (STATES) {  // nothing but the next chunk's decays
                 if (ok && c > 0) ok = bar_wait(bar_o, (c - 1) & 1, spin);
+                if (!ok) misc[1] = 1;
                 if (w >= 2 && c + 1 < nchunks) scan(c + 1);
                 continue;
             }
@@ -284,6 +282,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 }
                 __syncwarp();
             }
+            if (!ok) misc[1] = 1;
         }
         if (!STATES && !abort && nchunks > 0) {
             if (ok) ok = bar_wait(bar_o, (nchunks - 1) & 1, spin);
@@ -327,7 +326,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         };
         const uint64_t dA = desc_mn(smem_u32(tA)), dB = desc_mn(smem_u32(tB));
         constexpr uint32_t kId = idesc(64, 0, 1), kId2 = idesc(128, 0, 1), kIdT2 = idesc(128, 1, 1);
-        // group barrier: what was written is ready for the products issued next
+        // group barrier: what was written is ready for the products issued next.  After a wait that ran
+        // out every thread walks on, without waiting and without loading, so that the barriers hold.
         auto meet = [&]() {
             fence_async_smem();
             fence_before();
@@ -339,44 +339,37 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         for (int c = 0; c < nchunks && !abort; ++c) {
             const uint32_t aK = smem_u32(sm + OFF_K + kTile * (c & 1));
             const int64_t tile = ((chunk0 + c) * p.H + h) * kTile;
-            // ---- S hi, lo; K S.  Whether to stop is voted on here (an expired wait makes the rest of its
-            // chunk's waits pass)
+            // ---- S hi, lo; K S
+            if (misc[1]) ok = 0;
             store_split(S, 0, tA, tB);
             store_split(S + 8, 1, tA, tB);
-            if (ok) ok = bar_wait(bar_s0 + 8 * (c % 3), (c / 3) & 1, spin);
-            if (ok) ok = bar_wait(bar_k0 + 8 * (c & 1), (c >> 1) & 1, spin);
-            if (c * kC + kC > len) zero_rows(sm + OFF_K + kTile * (c & 1), len - c * kC, tid - 128, 128);
-            fence_async_smem();
-            fence_before();
-            if (named_sync_or(2, 128, !ok || misc[1])) {
-                abort = 1;
-                break;
+            if (c * kC + kC > len) {  // the last chunk's rows past the end
+                if (ok) ok = bar_wait(bar_k0 + 8 * (c & 1), (c >> 1) & 1, spin);
+                zero_rows(sm + OFF_K + kTile * (c & 1), len - c * kC, tid - 128, 128);
             }
-            fence_after();
+            meet();
             if (warp == 4) {
                 const uint64_t dK = desc_k(aK);
+                if (ok) ok = bar_wait_spin(bar_k0 + 8 * (c & 1), (c >> 1) & 1, spin * 64u);
+                __syncwarp();
                 if (elect_one()) {
                     mma_tile<kStepK, kStepMn, false>(tbase + COL_X, dK, dA, kId2);
                     mma_commit(bar_x);
                 }
-                __syncwarp();
-            } else if (warp == 5 && lane == 0) {
-                if (!STATES) {
-                    bar_arrive(bar_sw);
-                } else {
-                    if (in_bounds(p.status, chunk0 + c, 1, p.nchunks)) bulk_store(p.states + tile, smem_u32(tA), kTile);
-                    bulk_commit();
-                    bulk_wait_read<0>();
-                    bar_arrive(bar_qs);
-                }
+            } else if (STATES && warp == 5 && lane == 0) {
+                if (in_bounds(p.status, chunk0 + c, 1, p.nchunks)) bulk_store(p.states + tile, smem_u32(tA), kTile);
+                bulk_commit();
+                bulk_wait_read<0>();
+                bar_arrive(bar_qs);
             } else if (warp == 7 && c > 0 && c + 1 < nchunks) {  // S is there: the chunk before is done with its tiles
-                if (elect_one()) {
+                if (elect_one() && ok) {
                     load_tile(&map_k, OFF_K + kTile * ((c + 1) & 1), hk, c + 1, bar_k0 + 8 * ((c + 1) & 1));
                     if (!STATES) load_tile(&map_q, OFF_Q + kTile * ((c + 1) & 1), hk, c + 1, bar_q0 + 8 * ((c + 1) & 1));
                 }
             }
             __syncwarp();
             // ---- W = beta (v - gamma K S)
+            if (ok) ok = bar_wait(bar_s0 + 8 * (c % 3), (c / 3) & 1, spin);
             const ChunkArrays &arr = reinterpret_cast<const ChunkArrays *>(sm + OFF_ARR)[c % 3];
             const float gam = arr.gamma[row], tail = arr.tail[row], bet = arr.beta[row], gC = arr.gamma[kC - 1];
             const P2 b2 = pk(bet, bet), bg = pk(-bet * gam, -bet * gam), t2 = pk(tail, tail), g2 = pk(gC, gC);
@@ -386,6 +379,9 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
+            // only now may Q S be issued: beside K S it would hold that up
+            if (!STATES && warp == 5 && lane == 0) bar_arrive(bar_sw);
+            __syncwarp();
             const bool token = c * kC + row < len;  // else another sequence's, or nothing
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -412,7 +408,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 }
                 __syncwarp();
             } else if (warp == 7 && c + 1 < nchunks) {
-                if (elect_one()) load_tile(&map_v, OFF_V, h, c + 1, bar_v);
+                if (elect_one() && ok) load_tile(&map_v, OFF_V, h, c + 1, bar_v);
                 __syncwarp();
             }
             // ---- U, and diag(tail) U hi, lo
@@ -440,23 +436,21 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     mma_commit(bar_x);
                 }
                 __syncwarp();
-            } else if (warp == 5 && lane == 0) {
-                if (!STATES) {
-                    bar_arrive(bar_uw);
-                } else {
-                    if (in_bounds(p.status, chunk0 + c, 1, p.nchunks)) bulk_store(p.us + tile, smem_u32(tC), kTile);
-                    bulk_commit();
-                    bulk_wait_read<0>();
-                    bar_arrive(bar_o);
-                }
+            } else if (STATES && warp == 5 && lane == 0) {
+                if (in_bounds(p.status, chunk0 + c, 1, p.nchunks)) bulk_store(p.us + tile, smem_u32(tC), kTile);
+                bulk_commit();
+                bulk_wait_read<0>();
+                bar_arrive(bar_o);
             } else if (warp == 7 && c + 2 < nchunks) {
-                if (elect_one()) load_t(c + 2);
+                if (elect_one() && ok) load_t(c + 2);
             }
             __syncwarp();
             // ---- S
             if (ok) ok = bar_wait(bar_x, xph, spin);
             xph ^= 1;
             fence_after();
+            if (!STATES && warp == 5 && lane == 0) bar_arrive(bar_uw);  // P U, likewise
+            __syncwarp();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 P2 x[8];
@@ -464,6 +458,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) S[8 * half + i] = fma2(g2, S[8 * half + i], x[i]);
             }
+            if (!ok) misc[1] = 1;  // and its waits pass from here on, in this thread and soon in all
         }
         if (STATES && warp == 5 && lane == 0) bulk_wait_all();
         if (abort) ok = 0;
