@@ -263,7 +263,7 @@ int rwkv_wkv6_backward_omega_bf16(int64_t B, int64_t T, int64_t H, int64_t N,
  *             sequences.  No initialisation needed, undefined afterwards; calls whose work
  *             overlaps need a workspace each.
  *   N must be 64.  Index arrays are 4-byte aligned; other rules and errors as above.
- * Accumulation is fp32 and the state is held in fp32 throughout.  bf16 sequences of 16 tokens
+ * Accumulation is fp32 and the state is held in fp32 throughout.  bf16 sequences of 28 tokens
  * or more (packed: on average) run in 64-token chunks on the tensor cores: there the output
  * is formed from bf16 operands, and every operand of the state from two bf16 terms (2^-16 of
  * its value).  Others run token by token in fp32.

@@ -16,7 +16,9 @@
 // tokens, added in a fixed order.  Value heads that share a key head write their shares of dq
 // and dk to the workspace and a second kernel adds them, also in a fixed order.
 //
-// Bound by the chain of one token; the tensor-core path serves bf16.
+// A segment's inputs are copied to shared memory (cp.async) while the one before it is walked.
+// Bound by the chain of one token (forward, again, backward): 1.4 us a token for 1 to 32 heads (2.5
+// with inputs loaded where they are used).  The tensor-core path serves bf16.
 #include "wkv_internal.cuh"
 
 namespace wkv {
@@ -26,11 +28,29 @@ constexpr int kN = 64;
 constexpr int kThreads = 256;
 constexpr int kSeg = 8;  // tokens between checkpoints
 constexpr int kPart = 2 * kN + 2;  // dq, dk, dbeta, dg of one token
-// shared memory, floats: states [kSeg][4][256][4], r [kSeg][64], partial sums [kSeg][8][kPart]
-constexpr int kSmemBytes = (kSeg * 4096 + kSeg * kN + kSeg * 8 * kPart) * 4;
+// shared memory, floats: states [kSeg][4][256][4], r [kSeg][64], partial sums [kSeg][8][kPart],
+// two buffers of a segment's g and beta [kSeg][2]; then two of its k, v, q, do [kSeg][4][64] of T
+constexpr int kSmemFloats = kSeg * 4096 + kSeg * kN + kSeg * 8 * kPart + 2 * kSeg * 2;
+template <typename T> constexpr int kSmemBytes = kSmemFloats * 4 + 2 * kSeg * 4 * kN * static_cast<int>(sizeof(T));
+static_assert(kSmemFloats % 4 == 0, "the inputs start on 16 bytes");
 
 __device__ __forceinline__ float rd(const float *p) { return *p; }
 __device__ __forceinline__ float rd(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void rd8(const float *p, float (&x)[8])
+{
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void rd8(const __nv_bfloat16 *p, float (&x)[8])
+{
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(y[i] << 16);
+        x[2 * i + 1] = __uint_as_float(y[i] & 0xFFFF0000u);
+    }
+}
 __device__ __forceinline__ void wr(float *p, float x) { *p = x; }
 __device__ __forceinline__ void wr(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -58,7 +78,8 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
                    T *__restrict__ dbeta)
 {
     extern __shared__ float sm[];
-    float *states = sm, *rs = sm + kSeg * 4096, *part = rs + kSeg * kN;
+    float *states = sm, *rs = sm + kSeg * 4096, *part = rs + kSeg * kN, *scalars = part + kSeg * 8 * kPart;
+    T *inputs = reinterpret_cast<T *>(sm + kSmemFloats);
     const int64_t n = blockIdx.x, seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = lane >> 2, row = 8 * rg;
     const int col = 8 * warp + 2 * (lane & 3);
@@ -75,15 +96,41 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
         const float2 x = p.s0 ? *reinterpret_cast<const float2 *>(p.s0 + base + (row + m) * kN + col) : make_float2(0.f, 0.f);
         S[m][0] = x.x, S[m][1] = x.y;
     }
+    // A segment's inputs, copied ahead (of the first pass over it, k and v alone); thread i < 16
+    // brings g or beta of one token, through a register.
+    float sc = 0.f;
+    auto stage = [&](int64_t sg, bool all) {
+        constexpr int kE = 16 / static_cast<int>(sizeof(T)), kQ = kN / kE;
+        const int per = (all ? 4 : 2) * kQ;
+        for (int i = tid; i < kSeg * per; i += kThreads) {
+            const int x = i / per, arr = i % per / kQ, c = i % kQ * kE;
+            const int64_t t = first + sg * kSeg + x;
+            if (sg * kSeg + x >= len) break;
+            const T *src = arr == 0 ? k : arr == 1 ? v : arr == 2 ? q : dout;
+            src += (t * (arr == 0 || arr == 2 ? p.Hk : p.H) + (arr == 0 || arr == 2 ? hk : h)) * kN + c;
+            T *dst = inputs + (((sg & 1) * kSeg + x) * 4 + arr) * kN + c;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                         "l"(src)
+                         : "memory");
+        }
+        if (tid < 2 * kSeg && sg * kSeg + tid / 2 < len)
+            sc = rd((tid & 1 ? beta : g) + (first + sg * kSeg + tid / 2) * p.H + h);
+    };
+    auto arrived = [&](int64_t sg) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (tid < 2 * kSeg) scalars[(sg & 1) * 2 * kSeg + tid] = tid & 1 ? sc : expf(sc);
+        __syncthreads();
+    };
     // one token forward: S becomes the state after it; r (this lane's two columns) is returned
-    auto step = [&](int64_t t, float (&r)[2]) {
-        const int64_t th = t * p.H + h;
-        const T *pk = k + (t * p.Hk + hk) * kN + row;
-        const float a = expf(rd(g + th)), b = rd(beta + th);
+    auto step = [&](int64_t sg, int i, float (&r)[2]) {
+        const T *in = inputs + ((sg & 1) * kSeg + i) * 4 * kN;
+        const float *ab = scalars + ((sg & 1) * kSeg + i) * 2;
+        const float a = ab[0], b = ab[1];
         float kk[8], ks[2] = {};
+        rd8(in + row, kk);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
-            kk[m] = rd(pk + m);
             ks[0] = fmaf(kk[m], S[m][0], ks[0]);
             ks[1] = fmaf(kk[m], S[m][1], ks[1]);
         }
@@ -92,8 +139,8 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
             ks[0] += __shfl_xor_sync(0xffffffffu, ks[0], d);
             ks[1] += __shfl_xor_sync(0xffffffffu, ks[1], d);
         }
-        r[0] = rd(v + th * kN + col) - a * ks[0];
-        r[1] = rd(v + th * kN + col + 1) - a * ks[1];
+        r[0] = rd(in + kN + col) - a * ks[0];
+        r[1] = rd(in + kN + col + 1) - a * ks[1];
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             S[m][0] = fmaf(kk[m], b * r[0], a * S[m][0]);
@@ -101,13 +148,16 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
         }
     };
     float r[2];
+    if (nseg > 0) stage(0, nseg == 1);
     for (int64_t sg = 0; sg < nseg; ++sg) {
+        arrived(sg);  // and the segment before has been read
+        if (sg + 1 < nseg) stage(sg + 1, sg + 2 == nseg);
         float *ck = p.ckpt + ((seg0 + sg) * p.H + h) * kN * kN;
 #pragma unroll
         for (int m = 0; m < 8; ++m)
             *reinterpret_cast<float2 *>(ck + (row + m) * kN + col) = make_float2(S[m][0], S[m][1]);
         if (sg + 1 < nseg)
-            for (int i = 0; i < kSeg; ++i) step(first + sg * kSeg + i, r);
+            for (int i = 0; i < kSeg; ++i) step(sg, i, r);
     }
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
@@ -118,6 +168,8 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
         const int64_t t0 = first + sg * kSeg;
         const int cnt = static_cast<int>(min(static_cast<int64_t>(kSeg), len - sg * kSeg));
         const float *ck = p.ckpt + ((seg0 + sg) * p.H + h) * kN * kN;
+        if (sg + 1 < nseg) arrived(sg);
+        if (sg > 0) stage(sg - 1, true);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {  // this thread's own elements, written above
             const float2 x = *reinterpret_cast<const float2 *>(ck + (row + m) * kN + col);
@@ -127,18 +179,20 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
             float4 *mine = reinterpret_cast<float4 *>(states) + i * 1024 + tid;
 #pragma unroll
             for (int m = 0; m < 4; ++m) mine[m * 256] = make_float4(S[2 * m][0], S[2 * m][1], S[2 * m + 1][0], S[2 * m + 1][1]);
-            step(t0 + i, r);
+            step(sg, i, r);
             if (rg == 0) *reinterpret_cast<float2 *>(rs + i * kN + col) = make_float2(r[0], r[1]);
         }
         __syncwarp();
         for (int i = cnt - 1; i >= 0; --i) {
-            const int64_t t = t0 + i, th = t * p.H + h;
+            const int64_t th = (t0 + i) * p.H + h;
             const float4 *mine = reinterpret_cast<const float4 *>(states) + i * 1024 + tid;
-            const float a = expf(rd(g + th)), b = rd(beta + th);
-            const T *pk = k + (t * p.Hk + hk) * kN + row, *pq = q + (t * p.Hk + hk) * kN + row;
-            const float d0 = rd(dout + th * kN + col), d1 = rd(dout + th * kN + col + 1);
+            const T *in = inputs + ((sg & 1) * kSeg + i) * 4 * kN;
+            const float *ab = scalars + ((sg & 1) * kSeg + i) * 2;
+            const float a = ab[0], b = ab[1], d0 = rd(in + 3 * kN + col), d1 = rd(in + 3 * kN + col + 1);
             const float2 rr = *reinterpret_cast<const float2 *>(rs + i * kN + col);
-            float kk[8], pdq[8], sp[8][2], du[2] = {};
+            float kk[8], qq[8], pdq[8], sp[8][2], du[2] = {};
+            rd8(in + row, kk);
+            rd8(in + 2 * kN + row, qq);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const float4 x = mine[m * 256];
@@ -146,10 +200,8 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
             }
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
-                kk[m] = rd(pk + m);
-                const float qq = p.scale * rd(pq + m);
-                D[m][0] = fmaf(qq, d0, D[m][0]);
-                D[m][1] = fmaf(qq, d1, D[m][1]);
+                D[m][0] = fmaf(p.scale * qq[m], d0, D[m][0]);
+                D[m][1] = fmaf(p.scale * qq[m], d1, D[m][1]);
                 du[0] = fmaf(kk[m], D[m][0], du[0]);
                 du[1] = fmaf(kk[m], D[m][1], du[1]);
                 pdq[m] = p.scale * (fmaf(kk[m], b * rr.x, sp[m][0]) * d0 + fmaf(kk[m], b * rr.y, sp[m][1]) * d1);
@@ -262,7 +314,7 @@ template <typename T> cudaError_t launch(const DeltaBwdArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev]) {  // racing first calls set the same attribute: harmless
-        e = cudaFuncSetAttribute(delta_walks_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        e = cudaFuncSetAttribute(delta_walks_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<T>);
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
@@ -271,7 +323,7 @@ template <typename T> cudaError_t launch(const DeltaBwdArgs &a, cudaStream_t s)
     float *share = f.H == f.Hk ? nullptr : ck + nck * f.H * kN * kN;
     const WalkParams p{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, f.scale, f.s0, a.dsT, a.ds0, ck,
                        share, share ? share + ntok * f.H * kN : nullptr, nck, f.status};
-    delta_walks_kernel<T><<<static_cast<unsigned>(f.nseq * f.H), kThreads, kSmemBytes, s>>>(
+    delta_walks_kernel<T><<<static_cast<unsigned>(f.nseq * f.H), kThreads, kSmemBytes<T>, s>>>(
         p, static_cast<const T *>(f.q), static_cast<const T *>(f.k), static_cast<const T *>(f.v),
         static_cast<const T *>(f.g), static_cast<const T *>(f.beta), static_cast<const T *>(a.dout),
         static_cast<T *>(a.dq), static_cast<T *>(a.dk), static_cast<T *>(a.dv), static_cast<T *>(a.dg),

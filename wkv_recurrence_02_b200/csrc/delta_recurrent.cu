@@ -6,13 +6,14 @@
 //   k_t S' = a (k_t S),   q_t S = a (q_t S_prev) + (q_t . k_t) u_t,   a = exp(g_t).
 //
 // The columns of S are independent of one another given k, so a warp owns 16 columns of one
-// head and keeps them in registers for the whole sequence: lane (rg, cq) holds rows 8 rg ..
-// 8 rg + 7 of columns 4 cq .. 4 cq + 3.  Sums over rows are three shuffles; no barrier, no
-// shared memory.  One block is the four warps of one (sequence, head).
+// head and keeps them in registers for the whole sequence.  One block is the four warps of one
+// (sequence, head).
 //
-// One decoded token is bound by the state's bytes: 16 KB in and 16 KB out for each head, all of
-// a warp's 4 KB loaded at once.  Long fp32 sequences are bound by the chain of one token
-// (two rounds of shuffles).
+// Two kernels.  A few tokens (decode) are bound by the state's bytes, 16 KB in and 16 KB out
+// for each head, all of a warp's 4 KB loaded at once: 256 sequences of 64 heads take 94 us, 5.8
+// TB/s.  There lane (rg, cq) holds rows 8 rg .. 8 rg + 7 of columns 4 cq .. 4 cq + 3, 16-byte
+// loads and stores of the state; sums over rows are three shuffles; no shared memory.  More
+// tokens are bound by the chain and the instructions of one token: see delta_walk_kernel.
 #include "wkv_internal.cuh"
 
 namespace wkv {
@@ -153,9 +154,240 @@ delta_recurrent_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nse
     }
 }
 
+// ---------------------------------------------------------------- many tokens
+// The same walk for longer sequences, bound by instructions and by the chain of one token (k S,
+// two rounds of shuffles, u, the update).  A lane holds 16 rows of two columns, the rows in
+// pairs, so that the products are two-wide instructions (fma.rn.f32x2) and a sum over rows has
+// two rounds of shuffles: 64 fma2 and 10 shuffles a token where the layout above has 128 fma
+// and 27.  Inputs come through shared memory (cp.async), kGroups - 1 groups of kGroup tokens
+// ahead, a ring to each warp: no barrier.  Measured, one sequence of 4 heads, 256 tokens fp32: 59 us
+// (0.2 us a token), against 127 with the kernel above (one token ahead, a miss's latency each).
+constexpr int kGroup = 4, kGroups = 4, kRing = kGroup * kGroups;
+constexpr int kRow = 2 * kN + 16;  // a token in the ring: q, k, the warp's 16 columns of v
+
+template <typename T> __device__ __forceinline__ void copy16(T *smem, const T *gmem)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(smem))),
+                 "l"(gmem)
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float sum2(uint64_t x)
+{
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+    return lo + hi;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Rows 16 i + 4 rg + 0 .. 3, i = 0 .. 3, of a vector, in pairs (lanes side by side read side by side).
+__device__ __forceinline__ void ld_rows(const float *p, int rg, uint64_t (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(p + 16 * i + 4 * rg);
+        x[2 * i] = w.x, x[2 * i + 1] = w.y;
+    }
+}
+__device__ __forceinline__ void ld_rows(const __nv_bfloat16 *p, int rg, uint64_t (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float f[4];
+        ld_n(p + 16 * i + 4 * rg, f);
+        x[2 * i] = pack2(f[0], f[1]), x[2 * i + 1] = pack2(f[2], f[3]);
+    }
+}
+__device__ __forceinline__ void ld2(const float *p, float (&x)[2])
+{
+    const float2 w = *reinterpret_cast<const float2 *>(p);
+    x[0] = w.x, x[1] = w.y;
+}
+__device__ __forceinline__ void ld2(const __nv_bfloat16 *p, float (&x)[2])
+{
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    x[0] = __uint_as_float(w << 16), x[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void st2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+}
+
+// One token for one lane: its rows of q and k, its columns of v, exp(g) and beta.
+struct WalkToken {
+    uint64_t q[8], k[8];
+    float v[2], a, b;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, const int32_t *__restrict__ offsets,
+                  int64_t nslots, const int32_t *__restrict__ slots, const T *__restrict__ q, const T *__restrict__ k,
+                  const T *__restrict__ v, const T *__restrict__ g, const T *__restrict__ beta, float scale,
+                  const float *s0, T *__restrict__ o, float *sT, int *status)
+{
+    const int64_t n = blockIdx.x, seq = n / H, h = n % H, hk = h / (H / Hk);
+    const int lane = threadIdx.x & 31, rg = lane >> 3, warp = threadIdx.x >> 5;
+    const int col = 16 * warp + 2 * (lane & 7);
+    int64_t first, len64;
+    sequence_span(offsets, seq, Tn, &first, &len64);
+    const int len = in_bounds(status, first, len64, B * Tn) ? static_cast<int>(len64) : 0;
+    const int64_t slot = sequence_slot(slots, seq, nslots, status);
+    const int64_t at = ((slot * H + h) * kN + 4 * rg) * kN + col;  // this lane's first state element
+    const bool has = slot >= 0 && in_bounds(status, (slot * H + h) * kN * kN, kN * kN, nslots * H * kN * kN);
+
+    __shared__ __align__(16) T ring[kThreads / 32][kRing][kRow];
+    // Copies: chunks of 16 bytes; q and k of kTok tokens at a time, a chunk a lane, then v.
+    constexpr int kE = 16 / static_cast<int>(sizeof(T)), kQ = kN / kE, kTok = 32 / (2 * kQ), kV = 16 / kE;
+    const int xq = lane / (2 * kQ), cq = lane % (2 * kQ), xv = lane / kV;
+    const T *pq = (cq < kQ ? q : k) + (first * Hk + hk) * kN + (cq % kQ) * kE;
+    const T *pv = v + (first * H + h) * kN + 16 * warp + (lane % kV) * kE;
+    auto fetch = [&](int t0) {  // tokens t0 .. t0 + kGroup - 1; always one commit: groups are counted by them
+#pragma unroll
+        for (int x = 0; x < kGroup; x += kTok) {
+            const int t = t0 + x + xq;
+            if (t < len) copy16(&ring[warp][t % kRing][cq * kE], pq + t * (Hk * kN));
+        }
+        if (xv < kGroup && t0 + xv < len)
+            copy16(&ring[warp][(t0 + xv) % kRing][2 * kN + (lane % kV) * kE], pv + (t0 + xv) * (H * kN));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // At most kGroups - 2 groups are under way after this.
+    auto arrived = [&] {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 2) : "memory");
+        __syncwarp();
+    };
+    // Lane i's g and beta of the 32 tokens from t, loaded 32 tokens ahead.
+    const T *gh = g + first * H + h, *bh = beta + first * H + h;
+    float ac = 0.f, bc = 0.f, gn = 0.f, bn = 0.f;
+    auto scalars = [&](int t) {
+        const bool in = t + lane < len;
+        gn = in ? ld1(gh + (t + lane) * H) : 0.f;
+        bn = in ? ld1(bh + (t + lane) * H) : 0.f;
+    };
+    auto load = [&](int t, WalkToken &x) {  // t = 0, 1, ... in turn, its group complete
+        const T *row = ring[warp][t % kRing];
+        ld_rows(row, rg, x.q);
+        ld_rows(row + kN, rg, x.k);
+        ld2(row + 2 * kN + 2 * (lane & 7), x.v);
+        if (t % 32 == 0) {
+            ac = expf(gn), bc = bn;
+            scalars(t + 32);
+        }
+        x.a = __shfl_sync(0xffffffffu, ac, t % 32);
+        x.b = __shfl_sync(0xffffffffu, bc, t % 32);
+    };
+
+    scalars(0);
+#pragma unroll
+    for (int j = 0; j < kGroups - 1; ++j) fetch(j * kGroup);
+    uint64_t S[2][8];  // [column][pair of rows]
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
+        if (s0 && has) {
+            const float *p = s0 + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
+            ld2(p, x);
+            ld2(p + kN, y);
+        }
+        S[0][m] = pack2(x[0], y[0]), S[1][m] = pack2(x[1], y[1]);
+    }
+    T *po = o + (first * H + h) * kN + col;
+    auto step = [&](int t, const WalkToken &x) {
+        uint64_t ks[2] = {}, qs[2] = {}, qk2 = 0;
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) ks[c] = fma2(x.k[m], S[c][m], ks[c]);
+        }
+        float r[2] = {sum2(ks[0]), sum2(ks[1])};
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            qk2 = fma2(x.q[m], x.k[m], qk2);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) qs[c] = fma2(x.q[m], S[c][m], qs[c]);
+        }
+        float w[2] = {sum2(qs[0]), sum2(qs[1])}, qk = sum2(qk2);
+        const uint64_t a2 = pack2(x.a, x.a);
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) S[c][m] = mul2(a2, S[c][m]);
+#pragma unroll
+        for (int d = 8; d < 32; d *= 2) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) r[c] += __shfl_xor_sync(0xffffffffu, r[c], d);
+            qk += __shfl_xor_sync(0xffffffffu, qk, d);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) w[c] += __shfl_xor_sync(0xffffffffu, w[c], d);
+        }
+        float out[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float u = x.b * (x.v[c] - x.a * r[c]);
+            const uint64_t u2 = pack2(u, u);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) S[c][m] = fma2(x.k[m], u2, S[c][m]);
+            out[c] = scale * fmaf(qk, u, x.a * w[c]);
+        }
+        if (rg == 0) st2(po + t * (H * kN), out[0], out[1]);
+    };
+    WalkToken x, y;
+    arrived();  // group 0
+    if (len > 0) load(0, x);
+    for (int t = 0; t < len; t += kGroup) {
+        __syncwarp();  // every lane has read the group whose place is taken
+        fetch(t + (kGroups - 1) * kGroup);
+        arrived();  // the group after this one
+#pragma unroll
+        for (int i = 0; i < kGroup; i += 2) {  // the next token's inputs load under this one's sums
+            if (t + i >= len) break;
+            if (t + i + 1 < len) load(t + i + 1, y);
+            step(t + i, x);
+            if (t + i + 1 >= len) break;
+            if (t + i + 2 < len) load(t + i + 2, x);
+            step(t + i + 1, y);
+        }
+    }
+    if (sT && has) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            float *p = sT + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
+            float x0, y0, x1, y1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(y0) : "l"(S[0][m]));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x1), "=f"(y1) : "l"(S[1][m]));
+            st2(p, x0, x1);
+            st2(p + kN, y0, y1);
+        }
+    }
+}
+
+// Shortest mean sequence that takes the second kernel.  First against second, bf16, us (B1 H4, B64
+// H32): 4 tokens 8.2 / 8.2, 28.7 / 30.7; 6 tokens 10.2 / 8.2, 34.8 / 34.8; 8 tokens 12.3 / 10.2,
+// 41.0 / 38.9.
+constexpr int64_t kWalkTokens = 5;
+
 template <typename T> cudaError_t launch(const DeltaArgs &a, cudaStream_t s)
 {
-    delta_recurrent_kernel<T><<<static_cast<unsigned>(a.nseq * a.H), kThreads, 0, s>>>(
+    const auto kernel = (a.offsets ? a.T / a.nseq : a.T) >= kWalkTokens ? delta_walk_kernel<T> : delta_recurrent_kernel<T>;
+    kernel<<<static_cast<unsigned>(a.nseq * a.H), kThreads, 0, s>>>(
         a.B, a.T, a.Hk, a.H, a.nseq, a.offsets, a.nslots, a.slots, static_cast<const T *>(a.q),
         static_cast<const T *>(a.k), static_cast<const T *>(a.v), static_cast<const T *>(a.g),
         static_cast<const T *>(a.beta), a.scale, a.s0, static_cast<T *>(a.o), a.sT, a.status);

@@ -348,11 +348,17 @@ int delta_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t 
     // blocks are numbered by (sequence, head); token, head and slot indices are 32-bit
     if (x > 0x7fffffffLL || BT > 0x7fffff00LL || z->nslots > 0x7fffffffLL || z->nseq > 0x7ffffffeLL)
         return fail(RWKV_ERR_SHAPE, "more than 2^31 (sequence, head) pairs, tokens or slots%s");
+    const int64_t chunks = packed ? T / 64 + nseq : B * ((T + 63) / 64);  // at most 2^32
+    if (H > 0 && chunks > 0x7fffffffLL / H) return fail(RWKV_ERR_SHAPE, "more than 2^31 (chunk, head) pairs%s");
     return RWKV_OK;
 }
 
-// Shortest mean sequence that takes the chunked kernel.
-constexpr int64_t kDeltaChunkedTokens = 16;
+// Shortest mean sequences of bf16 that take the tensor cores; shorter ones and fp32 are walked
+// token by token.  A chunk costs the same however few tokens it holds, a walk grows with them.
+// Forward, walk against chunked, us (B1 H4, B8 H32, B64 H32): 24 tokens 14 / 16, 18 / 20, 76 / 76;
+// 32 tokens 16 / 16, 22 / 20, 96 / 78.  Backward: 8 tokens 14 / 31, 27 / 39, 158 / 172; 12 tokens
+// 22 / 31, 43 / 41, 256 / 172.
+constexpr int64_t kDeltaChunkedTokens = 28, kDeltaBwdChunkedTokens = 10;
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
@@ -366,9 +372,9 @@ wkv::DeltaArgs delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t H, const De
     return a;
 }
 
-bool delta_chunked(int64_t T, const DeltaSizes &z, bool packed, bool bf16)
+bool delta_chunked(int64_t T, const DeltaSizes &z, bool packed, bool bf16, int64_t least)
 {
-    return bf16 && z.n > 0 && z.nseq > 0 && (packed ? T / z.nseq : T) >= kDeltaChunkedTokens;
+    return bf16 && z.n > 0 && z.nseq > 0 && (packed ? T / z.nseq : T) >= least;
 }
 
 int delta_fwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t nseq, bool packed, int64_t nslots,
@@ -377,7 +383,7 @@ int delta_fwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int6
     int rc = delta_sizes(B, T, Hk, H, N, nseq, packed, nslots, slots, z);
     if (rc) return rc;
     const wkv::DeltaArgs a = delta_shape(B, T, Hk, H, *z, packed, bf16);
-    *bytes = N == 64 && delta_chunked(T, *z, packed, bf16) ? wkv::delta_t_bytes(a) : 0;
+    *bytes = N == 64 && delta_chunked(T, *z, packed, bf16, kDeltaChunkedTokens) ? wkv::delta_t_bytes(a) : 0;
     return RWKV_OK;
 }
 
@@ -437,12 +443,12 @@ int delta_bwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int6
     int rc = delta_sizes(B, T, Hk, H, N, nseq, packed, 0, false, z);
     if (rc) return rc;
     int64_t per, all;  // the largest workspace: a 64 x 64 fp32 state every 8 tokens and two fp32 shares
-    if (!mul_ok(T / 8 + z->nseq + 2, H, &per) || !mul_ok(per, B > 0 ? B : 1, &all) || !mul_ok(all, 8192, &all))
+    if (!mul_ok(T / 8 + z->nseq + 2, H, &per) || !mul_ok(per, B > 0 ? B : 1, &all) || !mul_ok(all, 1 << 16, &all))
         return fail(RWKV_ERR_SHAPE, "workspace size overflows%s");
     const wkv::DeltaArgs a = delta_shape(B, T, Hk, H, *z, packed, bf16);
     *bytes = z->nseq == 0 || z->nh == 0 || N != 64 ? 0
-             : delta_chunked(T, *z, packed, bf16)  ? wkv::delta_backward_tc_workspace_bytes(a)
-                                                   : wkv::delta_walks_workspace_bytes(a);
+             : delta_chunked(T, *z, packed, bf16, kDeltaBwdChunkedTokens) ? wkv::delta_backward_tc_workspace_bytes(a)
+                                                                          : wkv::delta_walks_workspace_bytes(a);
     return RWKV_OK;
 }
 
@@ -494,7 +500,7 @@ int delta_bwd_entry(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, cons
     a.f = wkv::DeltaArgs{B, T, Hk, H, z.nseq, offsets, z.nseq, nullptr, q, k, v, g, beta, scale, s0, nullptr, nullptr, bf16, status};
     a.dout = dout, a.dsT = dsT, a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.ds0 = ds0;
     a.workspace = workspace;
-    const cudaError_t err = delta_chunked(T, z, offsets != nullptr, bf16)
+    const cudaError_t err = delta_chunked(T, z, offsets != nullptr, bf16, kDeltaBwdChunkedTokens)
                                 ? wkv::delta_backward_tc_launch(a, tl_stream)
                                 : wkv::delta_backward_walks_launch(a, tl_stream);
     return err == cudaSuccess ? RWKV_OK : cuda_fail(err, "delta backward launch");
