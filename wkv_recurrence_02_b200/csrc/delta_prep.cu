@@ -27,7 +27,9 @@ using namespace dtc;
 constexpr int kThreads = 128;
 // shared memory: K tile, L blocks, per warp the diagonal block of L by columns and then D, T10
 // (a block of L, D or T is 1 KB: hi, then lo, 16 bytes for every lane as a B operand), decays
-constexpr int OFF_L = kTile, OFF_X = OFF_L + 6 * 1024, OFF_T10 = OFF_X + 4 * 1024;
+// a diagonal block: L by columns of 20 floats (no two of a warp's stores meet in a bank), then D
+constexpr int kXRow = 20, kXBytes = 16 * kXRow * 4;
+constexpr int OFF_L = kTile, OFF_X = OFF_L + 6 * 1024, OFF_T10 = OFF_X + 4 * kXBytes;
 constexpr int OFF_PN = OFF_T10 + 1024;     // [64] sums of log2 decays inside the block: integer part
 constexpr int OFF_PF = OFF_PN + 256;       // [64] fraction part
 constexpr int OFF_CF = OFF_PF + 256;       // [64] decay from after the token to its block's end
@@ -187,10 +189,10 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
             uint32_t a[4];
             ldmatrix4(a, base + swz(16 * w + g8 + 8 * (sel & 1), 32 * ks + 16 * (sel >> 1)));
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j >= w) {
+            for (int j = 0; j < 4; ++j)  // acc[j]: block column w + j
+                if (w + j < 4) {
                     uint32_t b[4];
-                    ldmatrix4(b, base + swz(16 * j + g8 + 8 * (sel >> 1), 32 * ks + 16 * (sel & 1)));
+                    ldmatrix4(b, base + swz(16 * (w + j) + g8 + 8 * (sel >> 1), 32 * ks + 16 * (sel & 1)));
                     mma16816(acc[j][0], a, b[0], b[1]);
                     mma16816(acc[j][1], a, b[2], b[3]);
                 }
@@ -199,7 +201,7 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     const int g = lane >> 2, t = lane & 3, r0 = 16 * w + g;
     // ---- L: the diagonal block by columns
     {
-        float *xt = reinterpret_cast<float *>(sm + OFF_X + 1024 * w);
+        float *xt = reinterpret_cast<float *>(sm + OFF_X + kXBytes * w);
         const float n0 = pn[r0], n1 = pn[r0 + 8], f0 = pf[r0], f1 = pf[r0 + 8], b0 = bt[r0], b1 = bt[r0 + 8];
 #pragma unroll
         for (int nn = 0; nn < 2; ++nn) {
@@ -207,13 +209,9 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
             const float2 ff = *reinterpret_cast<const float2 *>(pf + 16 * w + 8 * nn + 2 * t);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float kk = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j == w) kk = acc[j][nn][e];
                 const int col = 8 * nn + 2 * t + (e & 1), row = g + 8 * (e >> 1);
                 const float gam = ex2_approx(((e >> 1 ? n1 : n0) - (e & 1 ? cn.y : cn.x)) + ((e >> 1 ? f1 : f0) - (e & 1 ? ff.y : ff.x)));
-                xt[col * 16 + row] = col < row ? (e >> 1 ? b1 : b0) * gam * kk : 0.f;
+                xt[col * kXRow + row] = col < row ? (e >> 1 ? b1 : b0) * gam * acc[0][nn][e] : 0.f;
             }
         }
     }
@@ -223,8 +221,9 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
         const float cf0 = cf[r0], cf1 = cf[r0 + 8];
         float mn = 0.f, mf = 0.f;
 #pragma unroll
-        for (int j = 1; j < 4; ++j) {
-            if (j <= w) continue;
+        for (int jj = 1; jj < 4; ++jj) {
+            const int j = w + jj;
+            if (j > 3) break;
             const float mid = ex2_approx(mn + mf);
             mn += bs[j];
             mf += bs[4 + j];
@@ -235,7 +234,7 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float s = mid * (r ? cf1 : cf0);
-                    split2(mul2(mul2(cc, pk(s, s)), pk(acc[j][nn][2 * r], acc[j][nn][2 * r + 1])), &f.h[2 * r + nn],
+                    split2(mul2(mul2(cc, pk(s, s)), pk(acc[jj][nn][2 * r], acc[jj][nn][2 * r + 1])), &f.h[2 * r + nn],
                            &f.l[2 * r + nn]);
                 }
             }
@@ -248,14 +247,14 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     // updates
     if (w >= 2) {
         const int blk = 2 * (w - 2) + (lane >> 4), j = lane & 15;
-        const float4 *xt = reinterpret_cast<const float4 *>(sm + OFF_X + 1024 * blk);
+        const float4 *xt = reinterpret_cast<const float4 *>(sm + OFF_X + kXBytes * blk);
         P2 x[8], la[8], lb[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = pk(2 * i == j ? 1.f : 0.f, 2 * i + 1 == j ? 1.f : 0.f);
         auto fetch = [&](int k, P2 (&l)[8]) {
 #pragma unroll
             for (int q = (k + 1) / 4; q < 4; ++q) {
-                const float4 v = xt[4 * k + q];
+                const float4 v = xt[kXRow / 4 * k + q];
                 l[2 * q] = pk(v.x, v.y);
                 l[2 * q + 1] = pk(v.z, v.w);
             }
@@ -279,7 +278,7 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2(x[i], &dh[i], &dl[i]);
         __syncwarp();
-        unsigned char *at = sm + OFF_X + 1024 * blk + 64 * (j & 7) + 8 * (j >> 3);
+        unsigned char *at = sm + OFF_X + kXBytes * blk + 64 * (j & 7) + 8 * (j >> 3);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             *reinterpret_cast<uint2 *>(at + 16 * q) = make_uint2(dh[q], dh[4 + q]);
@@ -294,7 +293,7 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     unsigned char *const tout = p.t_out + (static_cast<int64_t>(id) * p.H + h) * kTBytes;
     if (!in_bounds(p.status, id, 1, p.nchunks)) return;
     auto L = [&](int k, int j) { return ld_block(sm + OFF_L + 1024 * (k * (k - 1) / 2 + j), lane); };
-    auto D = [&](int j) { return ld_block(sm + OFF_X + 1024 * j, lane); };
+    auto D = [&](int j) { return ld_block(sm + OFF_X + kXBytes * j, lane); };
     auto put = [&](int i, int j, const Frag &f) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
