@@ -263,6 +263,8 @@ int rwkv_wkv6_backward_omega_bf16(int64_t B, int64_t T, int64_t H, int64_t N,
  *             sequences.  No initialisation needed, undefined afterwards; calls whose work
  *             overlaps need a workspace each.
  *   N must be 64.  Index arrays are 4-byte aligned; other rules and errors as above.
+ *   Inputs of the tokens that sequences hold are finite (g may be -inf).  One that is not may
+ *   reach the outputs of up to 63 tokens before it too: give padding tokens zeros.
  * Accumulation is fp32 and the state is held in fp32 throughout.  bf16 sequences of 28 tokens
  * or more (packed: on average) run in 64-token chunks on the tensor cores: there the output
  * is formed from bf16 operands, and every operand of the state from two bf16 terms (2^-16 of
@@ -398,8 +400,8 @@ int rwkv_wkv6_forward_bf16_noalloc(int64_t B, int64_t T, int64_t H, int64_t N,
                                    const uint16_t *w, const float *u, const float *s0,
                                    uint16_t *y, float *sT, int segments);
 
-/* Test hook for the failure path (process-wide).  While enabled, every chunked WKV-6
- * launch first waits on a barrier that nothing signals, with a short bound; the wait
+/* Test hook for the failure path (process-wide).  While enabled, every chunked WKV-6 and
+ * every chunked delta-rule walk first waits on a barrier that nothing signals, with a short bound; the wait
  * runs out, the kernel records RWKV_ERR_TIMEOUT in the device status word, releases its
  * resources and returns without computing (outputs are then unspecified).  No fault or
  * hang is involved.  Returns the previous setting. */

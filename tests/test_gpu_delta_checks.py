@@ -1,0 +1,97 @@
+"""The bounds-checked debug build on the edge shapes of the delta-rule and state-pool kernels, and
+the failure path of the chunked ones.
+
+In the debug build a failed index check skips the access and records RWKV_ERR_BOUNDS in the
+device status word; these calls have to leave it at 0 and give the values of the 64-bit
+reference (tolerances: those of test_gpu_delta.py, derived there).
+"""
+import os
+
+import pytest
+import torch
+
+import delta_ref as ref
+from test_gpu_delta import BF16, F32, _args, _check_backward, _check_forward, _cu
+from wkv_recurrence_02_b200 import build, ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def debug_lib():
+    if not os.path.exists(build.LIB_DEBUG):
+        build.build(debug_bounds=True)
+    with ops.using_library(build.LIB_DEBUG) as lib:
+        assert lib.rwkv_debug_bounds() == 1
+        assert ops.device_status() == 0
+        yield lib
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,Hk,H", [(2, 1, 1, 2), (3, 7, 2, 2), (1, 27, 1, 3), (2, 28, 2, 2), (2, 65, 1, 2), (1, 300, 2, 2)])
+def test_debug_forward(debug_lib, dtype, B, T, Hk, H):
+    _check_forward(ref.inputs(B, T, Hk, H, dtype, seed=T), dtype=dtype)
+
+
+PACKED = [([5, 0, 1, 64, 3], 0, 0), ([65, 130, 0], 2, 3), ([1, 1, 1, 1], 0, 4), ([0, 63, 129, 0, 1], 1, 70)]
+
+
+def _packed(lens, lead, tail, dtype):
+    x = ref.inputs(1, lead + sum(lens) + tail, 1, 2, dtype, seed=len(lens), nseq=len(lens))
+    spans = ref.spans_of(lens, lead)
+    return x, spans, [a for a, _ in spans] + [lead + sum(lens)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,lead,tail", PACKED)
+def test_debug_forward_packed(debug_lib, dtype, lens, lead, tail):
+    x, spans, offsets = _packed(lens, lead, tail, dtype)
+    _check_forward(x, spans, offsets, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,Hk,H", [(2, 1, 1, 2), (1, 9, 2, 2), (2, 10, 1, 2), (1, 65, 2, 2), (2, 200, 1, 3)])
+def test_debug_backward(debug_lib, dtype, B, T, Hk, H):
+    _check_backward(ref.inputs(B, T, Hk, H, dtype, seed=T), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,lead,tail", PACKED[:2] + PACKED[3:])
+def test_debug_backward_packed(debug_lib, dtype, lens, lead, tail):
+    x, spans, offsets = _packed(lens, lead, tail, dtype)
+    _check_backward(x, dtype, spans, offsets)
+
+
+@pytest.mark.parametrize("shape,dim", [((6, 4), 0), ((3, 33, 5, 64), 1), ((40, 12004), 0)])
+def test_debug_pool(debug_lib, shape, dim):
+    gen = torch.Generator().manual_seed(sum(shape))
+    pool, P = torch.randn(*shape, generator=gen), shape[dim]
+    src = torch.randint(-1, P, (P,), generator=gen).tolist()
+    dst = torch.randint(-1, P, (P,), generator=gen).tolist()
+    got = pool.cuda()
+    ops.state_copy(got, *(torch.tensor(i, dtype=torch.int32, device="cuda") for i in (src, dst)), slot_dim=dim)
+    assert torch.equal(got.cpu(), ref.copied(pool, src, dst, dim))
+    live = torch.rand(P, generator=gen) < 0.6
+    got = pool.cuda()
+    new, count = ops.state_compact(got, live.cuda(), slot_dim=dim)
+    n = int(live.sum())
+    assert ops.device_status() == 0 and int(count) == n
+    assert torch.equal(got.cpu().narrow(dim, 0, n), pool.index_select(dim, live.nonzero()[:, 0]))
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_context_survives():
+    """The wait is made to run out on the host's word: a barrier that nothing signals."""
+    lib = ops.load()
+    x = ref.inputs(1, 200, 2, 2, BF16, seed=3)
+    d = _cu(x)
+    for call in (lambda: ops.delta_forward(*_args(d), s0=d["s0"]), lambda: ops.delta_backward(*_args(d), d["do"])):
+        assert ops.device_status() == 0
+        prev = lib.rwkv_debug_inject_timeout(1)
+        try:
+            call()
+            status = ops.device_status()
+        finally:
+            lib.rwkv_debug_inject_timeout(prev)
+        assert status == -6
+        _check_forward(x)
+        _check_backward(x, BF16)

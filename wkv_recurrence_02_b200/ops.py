@@ -437,7 +437,8 @@ def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=Non
     1/sqrt(N).  offsets: int32 [sequences+1], the runs of tokens of a packed call (B = 1).
     s0: [sequences,H,N,N] fp32 or None (zero); with slots (int32 [sequences]), a pool
     [P,H,N,N] whose slot slots[i] is sequence i's state, updated in place unless another pool
-    is given as sT; a negative slot is a sequence without a state.  Returns (o, sT), or o.
+    is given as sT; a negative slot is a sequence without a state.  Returns (o, sT), or o; an o
+    allocated here is not set for tokens outside every sequence.
     """
     lib = load()
     B, T, Hk, H, N, nseq, dt = _delta_shapes(q, k, v, g, beta, offsets)
