@@ -124,6 +124,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     __syncthreads();
     fence_after();
     const uint32_t tbase = misc[0];
+    // The backward pass's other walk needs nothing of this one and may start beside it.
+    if (STATES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     auto load_tile = [&](const CUtensorMap *map, uint32_t off, int64_t head, int c, uint32_t bar) {
         if (!tma_coord_ok(p.status, 0, 2, kN, row_t + static_cast<int64_t>(c) * kC, p.T)) return;
