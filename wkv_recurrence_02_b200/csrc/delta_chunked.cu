@@ -144,8 +144,12 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 load_tile(&map_k, OFF_K + kTile * c, hk, c, bar_k0 + 8 * c);
                 if (!STATES) load_tile(&map_q, OFF_Q + kTile * c, hk, c, bar_q0 + 8 * c);
                 if (c < 1) load_tile(&map_v, OFF_V, h, c, bar_v);
-                load_t(c);
             }
+            __syncwarp();
+        }
+        if (!STATES) asm volatile("griddepcontrol.wait;" ::: "memory");  // T's kernel is done
+        for (int c = 0; c < 2 && c < nchunks; ++c) {
+            if (elect_one()) load_t(c);
             __syncwarp();
         }
     }
@@ -513,8 +517,18 @@ cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cu
                    a.scale, a.s0, static_cast<__nv_bfloat16 *>(a.o), a.sT, static_cast<unsigned char *>(states),
                    static_cast<unsigned char *>(us), a.status, g_chunked_inject_timeout ? 100u : 100000u,
                    g_chunked_inject_timeout};
-    kern<<<static_cast<unsigned>(a.nseq * a.H), kThreads, kSmemBytes, s>>>(mq, mk, mv, p);
-    return cudaGetLastError();
+    // The forward walk may start (barriers, tensor memory, the first tiles) while T's kernel still runs.
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.nseq * a.H));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cfg.attrs = early;
+    cfg.numAttrs = STATES ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p);
 }
 }  // namespace
 

@@ -136,6 +136,7 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31;
     const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the walk waits for this grid itself
     const uint32_t heads = static_cast<uint32_t>(p.H), id = blockIdx.x / heads;
     const int64_t h = blockIdx.x % heads, hk = static_cast<uint32_t>(h) / (heads / static_cast<uint32_t>(p.Hk));
     int64_t seq, first, len;
