@@ -156,14 +156,15 @@ delta_recurrent_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nse
 
 // ---------------------------------------------------------------- many tokens
 // The same walk for longer sequences, bound by instructions and by the chain of one token (k S,
-// two rounds of shuffles, u, the update).  A lane holds 16 rows of two columns, the rows in
-// pairs, so that the products are two-wide instructions (fma.rn.f32x2) and a sum over rows has
-// two rounds of shuffles: 64 fma2 and 10 shuffles a token where the layout above has 128 fma
-// and 27.  Inputs come through shared memory (cp.async), kGroups - 1 groups of kGroup tokens
-// ahead, a ring to each warp: no barrier.  Measured, one sequence of 4 heads, 256 tokens fp32: 59 us
-// (0.2 us a token), against 127 with the kernel above (one token ahead, a miss's latency each).
+// two rounds of shuffles, u, the update).  A lane holds 16 rows of two columns (COLS; of one, where
+// there are few heads), the rows in pairs, so that the products are two-wide instructions
+// (fma.rn.f32x2) and a sum over rows has two rounds of shuffles: 64 fma2 and 10 shuffles a token
+// where the layout above has 128 fma and 27.  Inputs come through shared memory (cp.async), kGroups - 1 groups of kGroup tokens
+// ahead, a ring to each warp: no barrier.  Measured, one sequence of 4 heads, 256 tokens fp32: 56 us
+// (0.2 us a token: one warp on each scheduler, a third of its cycles issue), against 127 with the
+// kernel above (one token ahead, a miss's latency each).
 constexpr int kGroup = 4, kGroups = 4, kRing = kGroup * kGroups;
-constexpr int kRow = 2 * kN + 16;  // a token in the ring: q, k, the warp's 16 columns of v
+template <int COLS> constexpr int kRow = 2 * kN + 8 * COLS;  // a token in the ring: q, k, the warp's columns of v
 
 template <typename T> __device__ __forceinline__ void copy16(T *smem, const T *gmem)
 {
@@ -214,38 +215,47 @@ __device__ __forceinline__ void ld_rows(const __nv_bfloat16 *p, int rg, uint64_t
         x[2 * i] = pack2(f[0], f[1]), x[2 * i + 1] = pack2(f[2], f[3]);
     }
 }
-__device__ __forceinline__ void ld2(const float *p, float (&x)[2])
+__device__ __forceinline__ void ldc(const float *p, float (&x)[1]) { x[0] = *p; }
+__device__ __forceinline__ void ldc(const __nv_bfloat16 *p, float (&x)[1]) { x[0] = __bfloat162float(*p); }
+__device__ __forceinline__ void ldc(const float *p, float (&x)[2])
 {
     const float2 w = *reinterpret_cast<const float2 *>(p);
     x[0] = w.x, x[1] = w.y;
 }
-__device__ __forceinline__ void ld2(const __nv_bfloat16 *p, float (&x)[2])
+__device__ __forceinline__ void ldc(const __nv_bfloat16 *p, float (&x)[2])
 {
     const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
     x[0] = __uint_as_float(w << 16), x[1] = __uint_as_float(w & 0xFFFF0000u);
 }
-__device__ __forceinline__ void st2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
-__device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y)
+__device__ __forceinline__ void stc(float *p, const float (&x)[1]) { *p = x[0]; }
+__device__ __forceinline__ void stc(__nv_bfloat16 *p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
+__device__ __forceinline__ void stc(float *p, const float (&x)[2])
 {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+    *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+}
+__device__ __forceinline__ void stc(__nv_bfloat16 *p, const float (&x)[2])
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x[0], x[1]);
 }
 
 // One token for one lane: its rows of q and k, its columns of v, exp(g) and beta.
-struct WalkToken {
+template <int COLS> struct WalkToken {
     uint64_t q[8], k[8];
-    float v[2], a, b;
+    float v[COLS], a, b;
 };
 
-template <typename T>
+template <typename T, int COLS>
 __global__ void __launch_bounds__(kThreads)
 delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, const int32_t *__restrict__ offsets,
                   int64_t nslots, const int32_t *__restrict__ slots, const T *__restrict__ q, const T *__restrict__ k,
                   const T *__restrict__ v, const T *__restrict__ g, const T *__restrict__ beta, float scale,
                   const float *s0, T *__restrict__ o, float *sT, int *status)
 {
-    const int64_t n = blockIdx.x, seq = n / H, h = n % H, hk = h / (H / Hk);
+    constexpr int kParts = 2 / COLS;  // blocks of a (sequence, head)
+    const int64_t n = blockIdx.x / kParts, seq = n / H, h = n % H, hk = h / (H / Hk);
     const int lane = threadIdx.x & 31, rg = lane >> 3, warp = threadIdx.x >> 5;
-    const int col = 16 * warp + 2 * (lane & 7);
+    const int col0 = 8 * COLS * (4 * static_cast<int>(blockIdx.x % kParts) + warp);  // the warp's first column
+    const int col = col0 + COLS * (lane & 7);
     int64_t first, len64;
     sequence_span(offsets, seq, Tn, &first, &len64);
     const int len = in_bounds(status, first, len64, B * Tn) ? static_cast<int>(len64) : 0;
@@ -253,12 +263,12 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
     const int64_t at = ((slot * H + h) * kN + 4 * rg) * kN + col;  // this lane's first state element
     const bool has = slot >= 0 && in_bounds(status, (slot * H + h) * kN * kN, kN * kN, nslots * H * kN * kN);
 
-    __shared__ __align__(16) T ring[kThreads / 32][kRing][kRow];
+    __shared__ __align__(16) T ring[kThreads / 32][kRing][kRow<COLS>];
     // Copies: chunks of 16 bytes; q and k of kTok tokens at a time, a chunk a lane, then v.
-    constexpr int kE = 16 / static_cast<int>(sizeof(T)), kQ = kN / kE, kTok = 32 / (2 * kQ), kV = 16 / kE;
+    constexpr int kE = 16 / static_cast<int>(sizeof(T)), kQ = kN / kE, kTok = 32 / (2 * kQ), kV = 8 * COLS / kE;
     const int xq = lane / (2 * kQ), cq = lane % (2 * kQ), xv = lane / kV;
     const T *pq = (cq < kQ ? q : k) + (first * Hk + hk) * kN + (cq % kQ) * kE;
-    const T *pv = v + (first * H + h) * kN + 16 * warp + (lane % kV) * kE;
+    const T *pv = v + (first * H + h) * kN + col0 + (lane % kV) * kE;
     auto fetch = [&](int t0) {  // tokens t0 .. t0 + kGroup - 1; always one commit: groups are counted by them
 #pragma unroll
         for (int x = 0; x < kGroup; x += kTok) {
@@ -282,11 +292,11 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
         gn = in ? ld1(gh + (t + lane) * H) : 0.f;
         bn = in ? ld1(bh + (t + lane) * H) : 0.f;
     };
-    auto load = [&](int t, WalkToken &x) {  // t = 0, 1, ... in turn, its group complete
+    auto load = [&](int t, WalkToken<COLS> &x) {  // t = 0, 1, ... in turn, its group complete
         const T *row = ring[warp][t % kRing];
         ld_rows(row, rg, x.q);
         ld_rows(row + kN, rg, x.k);
-        ld2(row + 2 * kN + 2 * (lane & 7), x.v);
+        ldc(row + 2 * kN + COLS * (lane & 7), x.v);
         if (t % 32 == 0) {
             ac = expf(gn), bc = bn;
             scalars(t + 32);
@@ -298,58 +308,63 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
     scalars(0);
 #pragma unroll
     for (int j = 0; j < kGroups - 1; ++j) fetch(j * kGroup);
-    uint64_t S[2][8];  // [column][pair of rows]
+    uint64_t S[COLS][8];  // [column][pair of rows]
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
-        float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
+        float x[COLS] = {}, y[COLS] = {};
         if (s0 && has) {
             const float *p = s0 + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
-            ld2(p, x);
-            ld2(p + kN, y);
+            ldc(p, x);
+            ldc(p + kN, y);
         }
-        S[0][m] = pack2(x[0], y[0]), S[1][m] = pack2(x[1], y[1]);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) S[c][m] = pack2(x[c], y[c]);
     }
     T *po = o + (first * H + h) * kN + col;
-    auto step = [&](int t, const WalkToken &x) {
-        uint64_t ks[2] = {}, qs[2] = {}, qk2 = 0;
+    auto step = [&](int t, const WalkToken<COLS> &x) {
+        uint64_t ks[COLS] = {}, qs[COLS] = {}, qk2 = 0;
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) ks[c] = fma2(x.k[m], S[c][m], ks[c]);
+            for (int c = 0; c < COLS; ++c) ks[c] = fma2(x.k[m], S[c][m], ks[c]);
         }
-        float r[2] = {sum2(ks[0]), sum2(ks[1])};
+        float r[COLS], w[COLS];
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) r[c] = sum2(ks[c]);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             qk2 = fma2(x.q[m], x.k[m], qk2);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) qs[c] = fma2(x.q[m], S[c][m], qs[c]);
+            for (int c = 0; c < COLS; ++c) qs[c] = fma2(x.q[m], S[c][m], qs[c]);
         }
-        float w[2] = {sum2(qs[0]), sum2(qs[1])}, qk = sum2(qk2);
+        float qk = sum2(qk2);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) w[c] = sum2(qs[c]);
         const uint64_t a2 = pack2(x.a, x.a);
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) S[c][m] = mul2(a2, S[c][m]);
+            for (int c = 0; c < COLS; ++c) S[c][m] = mul2(a2, S[c][m]);
 #pragma unroll
         for (int d = 8; d < 32; d *= 2) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) r[c] += __shfl_xor_sync(0xffffffffu, r[c], d);
+            for (int c = 0; c < COLS; ++c) r[c] += __shfl_xor_sync(0xffffffffu, r[c], d);
             qk += __shfl_xor_sync(0xffffffffu, qk, d);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) w[c] += __shfl_xor_sync(0xffffffffu, w[c], d);
+            for (int c = 0; c < COLS; ++c) w[c] += __shfl_xor_sync(0xffffffffu, w[c], d);
         }
-        float out[2];
+        float out[COLS];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < COLS; ++c) {
             const float u = x.b * (x.v[c] - x.a * r[c]);
             const uint64_t u2 = pack2(u, u);
 #pragma unroll
             for (int m = 0; m < 8; ++m) S[c][m] = fma2(x.k[m], u2, S[c][m]);
             out[c] = scale * fmaf(qk, u, x.a * w[c]);
         }
-        if (rg == 0) st2(po + t * (H * kN), out[0], out[1]);
+        if (rg == 0) stc(po + t * (H * kN), out);
     };
-    WalkToken x, y;
+    WalkToken<COLS> x, y;
     arrived();  // group 0
     if (len > 0) load(0, x);
     for (int t = 0; t < len; t += kGroup) {
@@ -370,11 +385,11 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             float *p = sT + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
-            float x0, y0, x1, y1;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(y0) : "l"(S[0][m]));
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(x1), "=f"(y1) : "l"(S[1][m]));
-            st2(p, x0, x1);
-            st2(p + kN, y0, y1);
+            float x[COLS], y[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) asm("mov.b64 {%0, %1}, %2;" : "=f"(x[c]), "=f"(y[c]) : "l"(S[c][m]));
+            stc(p, x);
+            stc(p + kN, y);
         }
     }
 }
@@ -384,10 +399,18 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
 // 41.0 / 38.9.
 constexpr int64_t kWalkTokens = 5;
 
+// Most (sequence, head) pairs whose walks take one column a lane, in two blocks each: fewer
+// instructions in a token's chain, as long as the blocks have an SM each.  Two columns against one,
+// us for 128 tokens: 64 pairs fp32 37 / 35, bf16 47 / 39; 128 pairs 39 / 45, 47 / 47; 256 pairs 53 / 80,
+// 64 / 72.
+constexpr int64_t kNarrowPairs = 74;
+
 template <typename T> cudaError_t launch(const DeltaArgs &a, cudaStream_t s)
 {
-    const auto kernel = (a.offsets ? a.T / a.nseq : a.T) >= kWalkTokens ? delta_walk_kernel<T> : delta_recurrent_kernel<T>;
-    kernel<<<static_cast<unsigned>(a.nseq * a.H), kThreads, 0, s>>>(
+    const int64_t pairs = a.nseq * a.H;
+    const bool walk = (a.offsets ? a.T / a.nseq : a.T) >= kWalkTokens, narrow = walk && pairs <= kNarrowPairs;
+    const auto kernel = narrow ? delta_walk_kernel<T, 1> : walk ? delta_walk_kernel<T, 2> : delta_recurrent_kernel<T>;
+    kernel<<<static_cast<unsigned>(narrow ? 2 * pairs : pairs), kThreads, 0, s>>>(
         a.B, a.T, a.Hk, a.H, a.nseq, a.offsets, a.nslots, a.slots, static_cast<const T *>(a.q),
         static_cast<const T *>(a.k), static_cast<const T *>(a.v), static_cast<const T *>(a.g),
         static_cast<const T *>(a.beta), a.scale, a.s0, static_cast<T *>(a.o), a.sT, a.status);
