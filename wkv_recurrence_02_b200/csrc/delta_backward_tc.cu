@@ -37,6 +37,8 @@ using namespace dtc;
 //   chain group (warps 4-7)  dS -> K dS -> dU -> T^T dU = dW -> K^T diag(-beta gamma) dW -> dS
 //   side group (warps 0-3)   what the chain adds but does not wait for: Q K^T, P, P^T dO, and
 //                            Q^T diag(scale gamma) dO, where the chain's last product accumulates
+// Measured: B8 T4096 H32 245 us; bound by the chain as the forward walk is (B8 T1024 H32: 70 us, tensor
+// pipe 35 % active, DRAM 37 %, issue 31 %).
 constexpr int kThreads = 256;
 // 13 tiles: K, Q and dO of two chunks, T (hi, lo), a pair for P hi/lo and then diag(scale gamma) dO
 // hi/lo, and the chain's A, B, C: dS hi/lo (A, B), dU hi/lo (B, C), diag(-beta gamma) dW hi/lo (A, B)
@@ -464,6 +466,10 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 // A2.  The loads of the next chunk start as soon as the second round of products is done.  dQ, dK and
 // dV of a whole chunk leave as tiles (from where A1, A2 and dW were): a row of a thread's own is 16
 // bytes, and stores of those were the kernel's largest use of the shared-memory pipe.
+//
+// Measured: B8 T4096 H32 332 us for 1.6 GB (448 with a block a chunk, direct stores and no load ahead);
+// B8 T1024 H32 91 us, DRAM 46 %, issue 42 %, shared-memory pipe 39 %: two chunks an SM, each waiting
+// for its own loads, products and barriers in turn.
 constexpr int kGThreads = 256;
 constexpr int GO_Q = 0, GO_K = 2 * kTile, GO_DW = 4 * kTile;  // + kTile * (item % 2)
 constexpr int GO_V = 6 * kTile, GO_DO = 7 * kTile, GO_U = 8 * kTile, GO_S = 9 * kTile, GO_DS = 10 * kTile;

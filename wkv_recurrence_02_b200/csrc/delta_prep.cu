@@ -18,6 +18,10 @@
 //
 // T is written as its two terms in the order in which the walking kernels hold it in shared memory;
 // a warp's store is one 128-byte line.
+//
+// Measured: 92 us for B8 T4096 H32 (402 MB: 4.4 TB/s); at B8 T1024 H32, where T stays in the L2, the
+// shared-memory pipe is 71 % busy (24 block operands and the substitution's columns a chunk), which
+// bounds it, and issue 45 %.
 #include "delta_tc.cuh"
 
 namespace wkv {
