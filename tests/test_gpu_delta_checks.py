@@ -95,3 +95,22 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_survives():
         assert status == -6
         _check_forward(x)
         _check_backward(x, BF16)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,Hk,H", [(1, 130, 37, 74), (1, 130, 25, 75), (3, 65, 32, 32), (5, 29, 20, 40), (2, 12, 75, 75)])
+def test_many_heads(dtype, B, T, Hk, H):
+    """Both sides of the choices by the number of (sequence, head) pairs."""
+    x = ref.inputs(B, T, Hk, H, dtype, seed=B + H)
+    _check_forward(x, dtype=dtype)
+    _check_backward(x, dtype)
+
+
+@pytest.mark.parametrize("H", [2, 16])
+def test_many_packed_sequences(H):
+    lens, lead = [40, 0, 1, 129, 64, 63, 65, 28, 200, 2], 3
+    x = ref.inputs(1, lead + sum(lens) + 5, 2, H, BF16, seed=H, nseq=len(lens))
+    spans = ref.spans_of(lens, lead)
+    offsets = [a for a, _ in spans] + [lead + sum(lens)]
+    _check_forward(x, spans, offsets)
+    _check_backward(x, BF16, spans, offsets)

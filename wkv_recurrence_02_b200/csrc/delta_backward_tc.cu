@@ -1003,7 +1003,7 @@ cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     e = delta_states_launch(f, ws + l.t, ws + l.states, ws + l.us, s);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(delta_bwd_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(delta_bwd_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLoneSmemBytes);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_bwd_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmemBytes);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_bwd_state_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(delta_bwd_grad_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -1022,7 +1022,7 @@ cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(f.nseq * f.H));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = 2 * f.nseq * f.H <= kLoneCtas ? kLoneSmemBytes : kSmemBytes;
     cfg.stream = s;
     cfg.attrs = beside;
     cfg.numAttrs = 1;

@@ -25,6 +25,10 @@
 // (B, C), diag(tail) U hi/lo (A, B) and U (C) in turn.  Tensor memory (256 columns): the chain's
 // accumulators (128) and, for two chunks, one that takes Q K^T and then the output.
 //
+// With few (sequence, head) pairs two CTAs take 32 of the 64 value columns each (NV): the columns of S
+// are independent given K, and half of them is half of the conversions.  Both terms of an operand
+// then lie in one tile, side by side, and Q S and P U take both too.
+//
 // The backward pass's first walk is the same kernel (STATES): without queries and outputs, it
 // leaves the bf16 state before every chunk and U, as images of their tiles.
 //
@@ -32,7 +36,7 @@
 // some 700 for each of the three products (256 to 450 of them the tensor core's) and the rest the
 // conversions between registers, shared and tensor memory; two CTAs on an SM take 6230 for a chunk
 // of each.  B8 T4096 H32: 210 us (STATES 185) after 92 for T; B8 T1024 H32: 64 us, tensor pipe 32 %
-// active, DRAM 36 %, issue 33 %.  Slower: loads issued by the output group (334 us a call against
+// active, DRAM 36 %, issue 33 %.  With 32 columns a CTA some 3900 cycles a chunk.  Slower: loads issued by the output group (334 us a call against
 // 309), a vote of the group after every wait, a warp that only issues.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records RWKV_ERR_TIMEOUT in the device
@@ -70,7 +74,8 @@ struct Params {
     int inject_timeout;
 };
 
-template <bool STATES>
+// STATES: the backward pass's walk.  NV: value columns of a CTA, 64 or, in two CTAs, 32.
+template <bool STATES, int NV>
 __global__ void __launch_bounds__(kThreads, 2)
 delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const Params p)
@@ -99,7 +104,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, see elect_one
-    const int64_t n = blockIdx.x, seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
+    const int64_t n = blockIdx.x / (kN / NV), seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
+    const int vcol = NV * static_cast<int>(blockIdx.x % (kN / NV));  // this CTA's first value column
     int64_t first_, len_;
     sequence_span(p.offsets, seq, p.T, &first_, &len_);
     const int first = static_cast<int>(first_), len = static_cast<int>(len_);  // fewer than 2^31 tokens in all
@@ -205,15 +211,16 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             return 1;
         };
         const uint32_t co = tbase + (static_cast<uint32_t>(32 * w) << 16) + COL_O;  // + 64 * (chunk % 2)
-        const int row = 16 * w + (lane & 15), col = 32 * (lane >> 4);  // its output row, first of 32 columns
+        const int row = 16 * w + (lane & 15), col = vcol + NV / 2 * (lane >> 4);  // its output row, first column
         auto store_o = [&](int c) {  // output rows of chunk c
-            P2 x[16];
-            tmem_ld_row(co + 64 * (c & 1), x);
+            P2 x[NV / 4];
+            if constexpr (NV == 64) tmem_ld_row(co + 64 * (c & 1), x);
+            else tmem_ld_sum16<16, 32>(co + 64 * (c & 1), x);
             const int tok = c * kC + row;
             if (tok < len && in_bounds(p.status, first + tok, 1, ntok)) {
                 uint4 *dst = reinterpret_cast<uint4 *>(p.o + (static_cast<int64_t>(first + tok) * p.H + h) * kN + col);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < NV / 16; ++i)
                     dst[i] = make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
             }
         };
@@ -307,26 +314,31 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // ------------------------------------------------------------------ chain group
         const int q = warp & 3;
         const uint32_t tl = tbase + (static_cast<uint32_t>(32 * q) << 16);
-        const int row = 16 * q + (lane & 15), col = 32 * (lane >> 4);  // its row, first of 32 columns
+        constexpr int kHalves = NV / 32;  // a thread's columns, 16 at a time
+        const int row = 16 * q + (lane & 15), col = NV / 2 * (lane >> 4);  // its row, first of 16 kHalves columns
         unsigned char *tA = sm + OFF_A, *tB = sm + OFF_B, *tC = sm + OFF_CC;
+        unsigned char *tA2 = NV == 64 ? tB : tA, *tB2 = NV == 64 ? tC : tB;  // of the low terms
         const int64_t nstate = p.nslots * p.H * kN * kN;
-        const int64_t sat = ((slot * p.H + h) * kN + row) * kN + col;
-        P2 S[16];
-        if (p.s0 && slot >= 0 && in_bounds(p.status, sat, 32, nstate)) {
+        const int64_t sat = ((slot * p.H + h) * kN + row) * kN + vcol + col;
+        P2 S[8 * kHalves];
+        if (p.s0 && slot >= 0 && in_bounds(p.status, sat, NV / 2, nstate)) {
             const float4 *src = reinterpret_cast<const float4 *>(p.s0 + sat);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4 * kHalves; ++i) {
                 const float4 x = src[i];
                 S[2 * i] = pk(x.x, x.y);
                 S[2 * i + 1] = pk(x.z, x.w);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = pk(0.f, 0.f);
+            for (int i = 0; i < 8 * kHalves; ++i) S[i] = pk(0.f, 0.f);
         }
-        const uint32_t at0 = swz(row, 2 * col);  // this thread's 32 columns of a tile: i-th 16 bytes
+        // this thread's columns of a tile: i-th 16 bytes, also of the low terms and of V
+        const uint32_t at0 = swz(row, 2 * col), av0 = swz(row, 2 * (vcol + col));
         auto at = [&](int i) { return at0 ^ static_cast<uint32_t>(16 * i); };
-        // half of them (16 columns) as two bf16 terms
+        auto at_lo = [&](int i) { return at(i) ^ (NV == 32 ? 64u : 0u); };
+        auto at_v = [&](int i) { return av0 ^ static_cast<uint32_t>(16 * i); };
+        // 16 of them as two bf16 terms, in two tiles or, of 32 columns, side by side in one
         auto store_split = [&](const P2 *x, int half, unsigned char *th, unsigned char *tlo) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -334,11 +346,11 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split2(x[4 * i + e], &a[e], &b[e]);
                 *reinterpret_cast<uint4 *>(th + at(2 * half + i)) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4 *>(tlo + at(2 * half + i)) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4 *>(tlo + at_lo(2 * half + i)) = make_uint4(b[0], b[1], b[2], b[3]);
             }
         };
         const uint64_t dA = desc_mn(smem_u32(tA)), dB = desc_mn(smem_u32(tB));
-        constexpr uint32_t kId = idesc(64, 0, 1), kId2 = idesc(128, 0, 1), kIdT2 = idesc(128, 1, 1);
+        constexpr uint32_t kId = idesc(64, 0, 1), kId2 = idesc(2 * NV, 0, 1), kIdT2 = idesc(2 * NV, 1, 1);
         // group barrier: what was written is ready for the products issued next.  After a wait that ran
         // out every thread walks on, without waiting and without loading, so that the barriers hold.
         auto meet = [&]() {
@@ -354,8 +366,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             const int64_t tile = ((chunk0 + c) * p.H + h) * kTile;
             // ---- S hi, lo; K S
             if (misc[1]) ok = 0;
-            store_split(S, 0, tA, tB);
-            store_split(S + 8, 1, tA, tB);
+#pragma unroll
+            for (int half = 0; half < kHalves; ++half) store_split(S + 8 * half, half, tA, tA2);
             if (c * kC + kC > len) {  // the last chunk's rows past the end
                 if (ok) ok = bar_wait(bar_k0 + 8 * (c & 1), (c >> 1) & 1, spin);
                 zero_rows(sm + OFF_K + kTile * (c & 1), len - c * kC, tid - 128, 128);
@@ -397,18 +409,18 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             __syncwarp();
             const bool token = c * kC + row < len;  // else another sequence's, or nothing
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < kHalves; ++half) {
                 P2 x[8];
-                tmem_ld_sum16(tl + COL_X + 16 * half, x);
+                tmem_ld_sum16<NV / 2, NV>(tl + COL_X + 16 * half, x);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint4 vv = make_uint4(0u, 0u, 0u, 0u);
-                    if (token) vv = *reinterpret_cast<const uint4 *>(sm + OFF_V + at(2 * half + i));
+                    if (token) vv = *reinterpret_cast<const uint4 *>(sm + OFF_V + at_v(2 * half + i));
                     const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[4 * i + e] = fma2(bg, x[4 * i + e], mul2(b2, unpack2(vw[e])));
                 }
-                store_split(x, half, tB, tC);
+                store_split(x, half, tB, tB2);
             }
             meet();
             if (warp == 4) {  // ---- U = T W
@@ -430,16 +442,17 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             xph ^= 1;
             fence_after();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < kHalves; ++half) {
                 P2 x[8];
-                tmem_ld_sum16(tl + COL_X + 16 * half, x);
+                tmem_ld_sum16<NV / 2, NV>(tl + COL_X + 16 * half, x);
+                if (NV == 32) store_split(x, half, tC, tC);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2 && NV == 64; ++i)
                     *reinterpret_cast<uint4 *>(tC + at(2 * half + i)) =
                         make_uint4(pack2(x[4 * i]), pack2(x[4 * i + 1]), pack2(x[4 * i + 2]), pack2(x[4 * i + 3]));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], t2);
-                store_split(x, half, tA, tB);
+                store_split(x, half, tA, tA2);
             }
             meet();
             if (warp == 4) {  // ---- K^T diag(tail) U
@@ -465,9 +478,9 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (!STATES && warp == 5 && lane == 0) bar_arrive(bar_uw);  // P U, likewise
             __syncwarp();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < kHalves; ++half) {
                 P2 x[8];
-                tmem_ld_sum16(tl + COL_X + 16 * half, x);
+                tmem_ld_sum16<NV / 2, NV>(tl + COL_X + 16 * half, x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) S[8 * half + i] = fma2(g2, S[8 * half + i], x[i]);
             }
@@ -476,10 +489,10 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (STATES && warp == 5 && lane == 0) bulk_wait_all();
         if (abort) ok = 0;
         if (!ok) misc[1] = 1;
-        if (ok && p.sT && slot >= 0 && in_bounds(p.status, sat, 32, nstate)) {
+        if (ok && p.sT && slot >= 0 && in_bounds(p.status, sat, NV / 2, nstate)) {
             float4 *dst = reinterpret_cast<float4 *>(p.sT + sat);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(lo(S[2 * i]), hi(S[2 * i]), lo(S[2 * i + 1]), hi(S[2 * i + 1]));
+            for (int i = 0; i < 4 * kHalves; ++i) dst[i] = make_float4(lo(S[2 * i]), hi(S[2 * i]), lo(S[2 * i + 1]), hi(S[2 * i + 1]));
         }
     }
 
@@ -506,7 +519,12 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 }  // namespace
 
 namespace {
-template <bool STATES>
+// Most (sequence, head) pairs that take two CTAs each, of 32 value columns: less to convert between
+// two products, as long as each CTA has an SM.  64 columns against 32, us: B1 T4096 H8 157 / 136, H64
+// 192 / 179; B1 T2048 H74 101 / 97; B2 T1024 H50 58 / 64.
+constexpr int64_t kNarrowPairs = 74;
+
+template <bool STATES, int NV>
 cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cudaStream_t s)
 {
     if (a.nseq * a.H == 0) return cudaSuccess;
@@ -514,8 +532,8 @@ cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cu
     if (!make_map(&mq, STATES ? a.k : a.q, a.B, a.T, a.Hk) || !make_map(&mk, a.k, a.B, a.T, a.Hk) ||
         !make_map(&mv, a.v, a.B, a.T, a.H))
         return cudaErrorInvalidValue;
-    auto kern = delta_chunked_kernel<STATES>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    auto kern = delta_chunked_kernel<STATES, NV>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLoneSmemBytes);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
@@ -529,9 +547,10 @@ cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cu
     early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.nseq * a.H));
+    const int64_t ctas = a.nseq * a.H * (kN / NV);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = (STATES ? 2 : 1) * ctas <= kLoneCtas ? kLoneSmemBytes : kSmemBytes;
     cfg.stream = s;
     cfg.attrs = early;
     cfg.numAttrs = STATES ? 0 : 1;
@@ -541,12 +560,13 @@ cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cu
 
 cudaError_t delta_chunked_launch(const DeltaArgs &a, const void *t, cudaStream_t s)
 {
-    return launch<false>(a, t, nullptr, nullptr, s);
+    return a.nseq * a.H <= kNarrowPairs ? launch<false, 32>(a, t, nullptr, nullptr, s)
+                                        : launch<false, 64>(a, t, nullptr, nullptr, s);
 }
 
 cudaError_t delta_states_launch(const DeltaArgs &a, const void *t, void *states, void *us, cudaStream_t s)
 {
-    return launch<true>(a, t, states, us, s);
+    return launch<true, 64>(a, t, states, us, s);
 }
 
 }  // namespace wkv

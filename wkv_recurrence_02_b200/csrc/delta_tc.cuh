@@ -68,6 +68,12 @@ __device__ __forceinline__ uint64_t udesc_plain(uint32_t addr, uint32_t lbo, uin
 __device__ __forceinline__ uint64_t desc_t(uint32_t addr) { return udesc_plain(addr, 1024, 128); }
 // read across them (T^T dU): K steps of 16 rows are 256 bytes
 __device__ __forceinline__ uint64_t desc_tt(uint32_t addr) { return udesc_plain(addr, 128, 1024); }
+// A grid (the backward pass's two walks together) that leaves every CTA an SM of its own asks for more
+// shared memory than half of one: else some are put in pairs where the kernel before still holds
+// other SMs (B1 T2048 H148 forward: 142 us, so 122).
+constexpr int64_t kLoneCtas = 148;
+constexpr int kLoneSmemBytes = 120 * 1024;
+
 // Chunks of a call are numbered through: sequences take disjoint runs, since each needs at most
 // one more than its share of the tokens.
 __host__ __device__ __forceinline__ int64_t first_chunk(bool packed, int64_t seq, int64_t first, int64_t T)
@@ -126,20 +132,20 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][4])
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// Two accumulators, 64 columns apart, added: threads 0-15 hold columns c .. c + 15, threads 16-31
-// c + 32 .. c + 47, each thread one lane, as pairs.
-__device__ __forceinline__ void tmem_ld_sum16(uint32_t taddr, P2 (&x)[8])
+// Two accumulators, APART columns apart, added: threads 0-15 hold columns c .. c + 15, threads 16-31
+// those HALF further on, each thread one lane, as pairs.
+template <int HALF = 32, int APART = 64> __device__ __forceinline__ void tmem_ld_sum16(uint32_t taddr, P2 (&x)[8])
 {
     uint32_t a[16], b[16];
 #define WKV_LD16(r, at)                                                                                              \
     asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "                                                         \
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 32;"                               \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;"                              \
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),   \
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),          \
                    "=r"(r[15])                                                                                       \
-                 : "r"(at))
+                 : "r"(at), "n"(HALF))
     WKV_LD16(a, taddr);
-    WKV_LD16(b, taddr + 64);
+    WKV_LD16(b, taddr + APART);
 #undef WKV_LD16
     tmem_wait_ld();
 #pragma unroll
