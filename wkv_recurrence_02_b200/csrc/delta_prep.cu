@@ -19,9 +19,10 @@
 // T is written as its two terms in the order in which the walking kernels hold it in shared memory;
 // a warp's store is one 128-byte line.
 //
-// Measured: 92 us for B8 T4096 H32 (402 MB: 4.4 TB/s); at B8 T1024 H32, where T stays in the L2, the
-// shared-memory pipe is 71 % busy (24 block operands and the substitution's columns a chunk), which
-// bounds it, and issue 45 %.
+// Measured: 158 thousand cycles, 84 to 91 us by the clock, for B8 T4096 H32 (402 MB, 4.4 to 4.8 TB/s;
+// 168 thousand before D's places were chosen against bank conflicts and the diagonal blocks of K K^T
+// took their B operand from the A one).  Issue is 60 % active, the shared-memory pipe about as busy
+// (24 block operands and the substitution's columns a chunk).
 #include "delta_tc.cuh"
 
 namespace wkv {
@@ -84,12 +85,16 @@ __device__ __forceinline__ Frag turn(const Frag &f)
     }
     return o;
 }
-__device__ __forceinline__ Frag ld_block(const unsigned char *block, int lane)
+// Where lane (g, t)'s 16 bytes of D lie: written column by column and read lane by lane, both without
+// two accesses in a bank.
+__device__ __forceinline__ int d_slot(int g, int t) { return 16 * (8 * t + (g ^ (2 * t))); }
+__device__ __forceinline__ Frag ld_at(const unsigned char *block, int at)
 {
-    const uint4 h = *reinterpret_cast<const uint4 *>(block + 16 * lane);
-    const uint4 l = *reinterpret_cast<const uint4 *>(block + 512 + 16 * lane);
+    const uint4 h = *reinterpret_cast<const uint4 *>(block + at);
+    const uint4 l = *reinterpret_cast<const uint4 *>(block + 512 + at);
     return {{h.x, h.y, h.z, h.w}, {l.x, l.y, l.z, l.w}};
 }
+__device__ __forceinline__ Frag ld_block(const unsigned char *block, int lane) { return ld_at(block, 16 * lane); }
 __device__ __forceinline__ void put_block(unsigned char *block, int lane, const Frag &f)
 {
     *reinterpret_cast<uint4 *>(block + 16 * lane) = make_uint4(f.h[0], f.h[1], f.h[2], f.h[3]);
@@ -194,7 +199,9 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
             uint32_t a[4];
             ldmatrix4(a, base + swz(16 * w + g8 + 8 * (sel & 1), 32 * ks + 16 * (sel >> 1)));
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // acc[j]: block column w + j
+            for (int nn = 0; nn < 2; ++nn) mma16816(acc[0][nn], a, a[nn], a[2 + nn]);  // as B: the same rows of K
+#pragma unroll
+            for (int j = 1; j < 4; ++j)  // acc[j]: block column w + j
                 if (w + j < 4) {
                     uint32_t b[4];
                     ldmatrix4(b, base + swz(16 * (w + j) + g8 + 8 * (sel >> 1), 32 * ks + 16 * (sel & 1)));
@@ -283,11 +290,11 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2(x[i], &dh[i], &dl[i]);
         __syncwarp();
-        unsigned char *at = sm + OFF_X + kXBytes * blk + 64 * (j & 7) + 8 * (j >> 3);
+        unsigned char *at = sm + OFF_X + kXBytes * blk + 8 * (j >> 3);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            *reinterpret_cast<uint2 *>(at + 16 * q) = make_uint2(dh[q], dh[4 + q]);
-            *reinterpret_cast<uint2 *>(at + 512 + 16 * q) = make_uint2(dl[q], dl[4 + q]);
+            *reinterpret_cast<uint2 *>(at + d_slot(j & 7, q)) = make_uint2(dh[q], dh[4 + q]);
+            *reinterpret_cast<uint2 *>(at + 512 + d_slot(j & 7, q)) = make_uint2(dl[q], dl[4 + q]);
         }
     }
     if (__syncthreads_or(!ok)) {
@@ -298,7 +305,7 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     unsigned char *const tout = p.t_out + (static_cast<int64_t>(id) * p.H + h) * kTBytes;
     if (!in_bounds(p.status, id, 1, p.nchunks)) return;
     auto L = [&](int k, int j) { return ld_block(sm + OFF_L + 1024 * (k * (k - 1) / 2 + j), lane); };
-    auto D = [&](int j) { return ld_block(sm + OFF_X + kXBytes * j, lane); };
+    auto D = [&](int j) { return ld_at(sm + OFF_X + kXBytes * j, d_slot(g, t)); };
     auto put = [&](int i, int j, const Frag &f) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
