@@ -265,7 +265,7 @@ int rwkv_wkv6_backward_omega_bf16(int64_t B, int64_t T, int64_t H, int64_t N,
  *   N must be 64.  Index arrays are 4-byte aligned; other rules and errors as above.
  *   Inputs of the tokens that sequences hold are finite (g may be -inf).  One that is not may
  *   reach the outputs of up to 63 tokens before it too: give padding tokens zeros.
- * Accumulation is fp32 and the state is held in fp32 throughout.  bf16 sequences of 28 tokens
+ * Accumulation is fp32 and the state is held in fp32 throughout.  bf16 sequences of 24 tokens
  * or more (packed: on average) run in 64-token chunks on the tensor cores: there the output
  * is formed from bf16 operands, and every operand of the state from two bf16 terms (2^-16 of
  * its value).  Others run token by token in fp32.

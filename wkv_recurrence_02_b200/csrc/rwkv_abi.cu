@@ -355,10 +355,10 @@ int delta_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t 
 
 // Shortest mean sequences of bf16 that take the tensor cores; shorter ones and fp32 are walked
 // token by token.  A chunk costs the same however few tokens it holds, a walk grows with them.
-// Forward, walk against chunked, us (B1 H4, B8 H32, B64 H32): 24 tokens 14 / 16, 18 / 20, 76 / 76;
-// 32 tokens 16 / 16, 22 / 20, 96 / 78.  Backward: 8 tokens 14 / 31, 27 / 39, 158 / 172; 12 tokens
-// 22 / 31, 43 / 41, 256 / 172.
-constexpr int64_t kDeltaChunkedTokens = 28, kDeltaBwdChunkedTokens = 10;
+// Forward, walk against chunked, us (B1 H4, B8 H32, B64 H32): 20 tokens 10 / 12, 16 / 16, 66 / 72; 28
+// tokens 12 / 12, 20 / 18, 86 / 74.  Backward: 8 tokens 14 / 25, 27 / 37, 156 / 166; 10 tokens 20 / 26,
+// 39 / 35, 233 / 166 (the walks' segments are of 8).
+constexpr int64_t kDeltaChunkedTokens = 24, kDeltaBwdChunkedTokens = 9;
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
