@@ -106,11 +106,23 @@ def test_many_heads(dtype, B, T, Hk, H):
     _check_backward(x, dtype)
 
 
-@pytest.mark.parametrize("H", [2, 16])
-def test_many_packed_sequences(H):
-    lens, lead = [40, 0, 1, 129, 64, 63, 65, 28, 200, 2], 3
+UNEVEN = [40, 0, 1, 129, 64, 63, 65, 28, 200, 2]
+
+
+@pytest.mark.parametrize("lens,H", [(UNEVEN, 2), (UNEVEN, 16), ([66, 64, 65, 1, 66], 20)])
+def test_many_packed_sequences(lens, H):
+    """Few and many pairs, of even and of uneven lengths."""
+    lead = 3
     x = ref.inputs(1, lead + sum(lens) + 5, 2, H, BF16, seed=H, nseq=len(lens))
     spans = ref.spans_of(lens, lead)
     offsets = [a for a, _ in spans] + [lead + sum(lens)]
     _check_forward(x, spans, offsets)
     _check_backward(x, BF16, spans, offsets)
+
+
+def test_most_packed_pairs():
+    """More pairs than the blocks look over for their lengths."""
+    lens = [24] * 519 + [25]
+    x = ref.inputs(1, sum(lens), 1, 2, BF16, seed=5, nseq=len(lens))
+    spans = ref.spans_of(lens)
+    _check_forward(x, spans, [a for a, _ in spans] + [sum(lens)])

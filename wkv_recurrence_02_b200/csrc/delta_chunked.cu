@@ -74,11 +74,10 @@ struct Params {
     int inject_timeout;
 };
 
-// STATES: the backward pass's walk.  NV: value columns of a CTA, 64 or, in two CTAs, 32.
+// The columns vcol .. vcol + NV - 1 of (sequence, head) number n.  STATES: the backward pass's walk.
 template <bool STATES, int NV>
-__global__ void __launch_bounds__(kThreads, 2)
-delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                     const __grid_constant__ CUtensorMap map_v, const Params p)
+__device__ __forceinline__ void walk(const CUtensorMap *map_q, const CUtensorMap *map_k, const CUtensorMap *map_v,
+                                     const Params &p, int64_t n, int vcol)
 {
     extern __shared__ unsigned char smem_raw[];
     // aligned by an offset on the __shared__ array itself (not through an integer), so the
@@ -104,8 +103,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, see elect_one
-    const int64_t n = blockIdx.x / (kN / NV), seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
-    const int vcol = NV * static_cast<int>(blockIdx.x % (kN / NV));  // this CTA's first value column
+    const int64_t seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
     int64_t first_, len_;
     sequence_span(p.offsets, seq, p.T, &first_, &len_);
     const int first = static_cast<int>(first_), len = static_cast<int>(len_);  // fewer than 2^31 tokens in all
@@ -154,9 +152,9 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     if (warp == 7) {
         for (int c = 0; c < 2 && c < nchunks; ++c) {
             if (elect_one()) {
-                load_tile(&map_k, OFF_K + kTile * c, hk, c, bar_k0 + 8 * c);
-                if (!STATES) load_tile(&map_q, OFF_Q + kTile * c, hk, c, bar_q0 + 8 * c);
-                if (c < 1) load_tile(&map_v, OFF_V, h, c, bar_v);
+                load_tile(map_k, OFF_K + kTile * c, hk, c, bar_k0 + 8 * c);
+                if (!STATES) load_tile(map_q, OFF_Q + kTile * c, hk, c, bar_q0 + 8 * c);
+                if (c < 1) load_tile(map_v, OFF_V, h, c, bar_v);
             }
             __syncwarp();
         }
@@ -388,8 +386,8 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 bar_arrive(bar_qs);
             } else if (warp == 7 && c > 0 && c + 1 < nchunks) {  // S is there: the chunk before is done with its tiles
                 if (elect_one() && ok) {
-                    load_tile(&map_k, OFF_K + kTile * ((c + 1) & 1), hk, c + 1, bar_k0 + 8 * ((c + 1) & 1));
-                    if (!STATES) load_tile(&map_q, OFF_Q + kTile * ((c + 1) & 1), hk, c + 1, bar_q0 + 8 * ((c + 1) & 1));
+                    load_tile(map_k, OFF_K + kTile * ((c + 1) & 1), hk, c + 1, bar_k0 + 8 * ((c + 1) & 1));
+                    if (!STATES) load_tile(map_q, OFF_Q + kTile * ((c + 1) & 1), hk, c + 1, bar_q0 + 8 * ((c + 1) & 1));
                 }
             }
             __syncwarp();
@@ -433,7 +431,7 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 }
                 __syncwarp();
             } else if (warp == 7 && c + 1 < nchunks) {
-                if (elect_one() && ok) load_tile(&map_v, OFF_V, h, c + 1, bar_v);
+                if (elect_one() && ok) load_tile(map_v, OFF_V, h, c + 1, bar_v);
                 __syncwarp();
             }
             // ---- U, and diag(tail) U hi, lo
@@ -516,13 +514,52 @@ delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols));
 }
 
-}  // namespace
-
-namespace {
 // Most (sequence, head) pairs that take two CTAs each, of 32 value columns: less to convert between
 // two products, as long as each CTA has an SM.  64 columns against 32, us: B1 T4096 H8 157 / 136, H64
 // 192 / 179; B1 T2048 H74 101 / 97; B2 T1024 H50 58 / 64.
 constexpr int64_t kNarrowPairs = 74;
+// Most pairs of a packed call that decides by its lengths: the pairs walking at a time are on average
+// the tokens over the longest sequence, times the heads, and that is what has to be few.  13
+// sequences of 0 to 2048 tokens, 6665 in all, H16: 106 us with 64 columns, 97 with 32.
+constexpr int64_t kPackedPairs = 1024;
+
+// Whether a packed call's pairs take two CTAs each.  All threads of the block; every block finds the same.
+__device__ __forceinline__ bool few_at_a_time(const Params &p)
+{
+    __shared__ unsigned warp_max[kThreads / 32], warp_sum[kThreads / 32];
+    unsigned most = 0, sum = 0;
+    for (int64_t i = threadIdx.x; i < p.nseq; i += kThreads) {
+        int64_t first, len;
+        sequence_span(p.offsets, i, p.T, &first, &len);
+        most = max(most, static_cast<unsigned>(len));
+        sum += static_cast<unsigned>(len);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = most, warp_sum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) {
+        most = w ? max(most, warp_max[w]) : warp_max[w];
+        sum = w ? sum + warp_sum[w] : warp_sum[w];
+    }
+    return static_cast<int64_t>(sum) * p.H <= kNarrowPairs * static_cast<int64_t>(most);
+}
+
+// NV: value columns of a CTA, 64 or, in two CTAs, 32; 0: as few_at_a_time says.
+template <bool STATES, int NV>
+__global__ void __launch_bounds__(kThreads, 2)
+delta_chunked_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const Params p)
+{
+    if constexpr (NV > 0) {
+        walk<STATES, NV>(&map_q, &map_k, &map_v, p, blockIdx.x / (kN / NV), NV * static_cast<int>(blockIdx.x % (kN / NV)));
+    } else {
+        const int64_t n = blockIdx.x / 2;
+        const int part = blockIdx.x % 2;
+        if (few_at_a_time(p)) walk<STATES, 32>(&map_q, &map_k, &map_v, p, n, 32 * part);
+        else if (part == 0) walk<STATES, 64>(&map_q, &map_k, &map_v, p, n, 0);
+    }
+}
 
 template <bool STATES, int NV>
 cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cudaStream_t s)
@@ -547,7 +584,7 @@ cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cu
     early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    const int64_t ctas = a.nseq * a.H * (kN / NV);
+    const int64_t ctas = a.nseq * a.H * (NV == 64 ? 1 : 2);
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (STATES ? 2 : 1) * ctas <= kLoneCtas ? kLoneSmemBytes : kSmemBytes;
@@ -560,8 +597,10 @@ cudaError_t launch(const DeltaArgs &a, const void *t, void *states, void *us, cu
 
 cudaError_t delta_chunked_launch(const DeltaArgs &a, const void *t, cudaStream_t s)
 {
-    return a.nseq * a.H <= kNarrowPairs ? launch<false, 32>(a, t, nullptr, nullptr, s)
-                                        : launch<false, 64>(a, t, nullptr, nullptr, s);
+    const int64_t pairs = a.nseq * a.H;
+    if (pairs <= kNarrowPairs) return launch<false, 32>(a, t, nullptr, nullptr, s);
+    if (a.offsets && pairs <= kPackedPairs) return launch<false, 0>(a, t, nullptr, nullptr, s);
+    return launch<false, 64>(a, t, nullptr, nullptr, s);
 }
 
 cudaError_t delta_states_launch(const DeltaArgs &a, const void *t, void *states, void *us, cudaStream_t s)
