@@ -7,18 +7,21 @@
 //   dq_t = scale S do_t^T,   du = k_t D,   dbeta_t = du . r_t,   dv_t = beta_t du
 //   dk_t = D u_t^T - S' dv_t^T,   D' = D - k_t^T dv_t,   dg_t = <D', S'>,   D = a_t D'.
 //
-// One block owns one (sequence, value head).  A forward pass leaves the state before every 8th
-// token in the workspace; the backward pass takes 8 tokens at a time, forms their states again
-// from that checkpoint (each thread keeps its own 16 elements of the 8 states in shared memory)
-// and then walks them in reverse.  Warp w owns columns 8 w .. 8 w + 7; lane (rg, cq) rows
-// 8 rg .. 8 rg + 7 of columns 2 cq, 2 cq + 1 of those.  Sums over rows are shuffles; sums over
-// columns (dq, dk, dbeta, dg) leave the block's eight warps through shared memory once per 8
-// tokens, added in a fixed order.  Value heads that share a key head write their shares of dq
-// and dk to the workspace and a second kernel adds them, also in a fixed order.
+// In segments of 8 tokens.  Two walks side by side (delta_recurrent.cu) leave the state before every
+// segment and D after it; then a block for each (segment, value head), all at once, forms the
+// segment's states and updates again and walks them in reverse.  Each thread keeps its own 16
+// elements of every fourth state in shared memory and forms those between once more: with the
+// updates known that takes no sums, and three blocks fit on an SM where all eight states leave room
+// for one.  Warp w owns columns 8 w .. 8 w + 7; lane (rg, cq) rows 8 rg .. 8 rg + 7
+// of columns 2 cq, 2 cq + 1 of those.  Sums over rows are shuffles; sums over columns (dq, dk,
+// dbeta, dg) leave the block's eight warps through shared memory once, added in a fixed order.
+// Value heads that share a key head write their shares of dq and dk to the workspace and a second
+// kernel adds them, also in a fixed order.
 //
-// A segment's inputs are copied to shared memory (cp.async) while the one before it is walked.
-// Bound by the chain of one token (forward, again, backward): 1.4 us a token for 1 to 32 heads (2.5
-// with inputs loaded where they are used).  The tensor-core path serves bf16.
+// Bound by the chain of one token in the two walks: 0.24 us a token (1024 tokens of 4 heads fp32 249
+// us, where one block walking all segments of a head in turn took 1366).  With many heads, by the
+// segments' instructions: 4 sequences of 128 tokens, 32 heads 147 us (181 with every state kept).  The
+// tensor-core path serves longer bf16 sequences.
 #include "wkv_internal.cuh"
 
 namespace wkv {
@@ -26,12 +29,14 @@ namespace {
 
 constexpr int kN = 64;
 constexpr int kThreads = 256;
-constexpr int kSeg = 8;  // tokens between checkpoints
+constexpr int kSeg = kDeltaSeg;
 constexpr int kPart = 2 * kN + 2;  // dq, dk, dbeta, dg of one token
-// shared memory, floats: states [kSeg][4][256][4], r [kSeg][64], partial sums [kSeg][8][kPart],
-// two buffers of a segment's g and beta [kSeg][2]; then two of its k, v, q, do [kSeg][4][64] of T
-constexpr int kSmemFloats = kSeg * 4096 + kSeg * kN + kSeg * 8 * kPart + 2 * kSeg * 2;
-template <typename T> constexpr int kSmemBytes = kSmemFloats * 4 + 2 * kSeg * 4 * kN * static_cast<int>(sizeof(T));
+constexpr int kKeep = 4;  // tokens between states kept
+// shared memory, floats: states [kSeg / kKeep][4][256][4], r [kSeg][64], partial sums [kSeg][8][kPart],
+// exp(g) and beta [kSeg][2]; then k, v, q, do [kSeg][4][64] of T
+constexpr int kStates = kSeg / kKeep * 4096;
+constexpr int kSmemFloats = kStates + kSeg * kN + kSeg * 8 * kPart + kSeg * 2;
+template <typename T> constexpr int kSmemBytes = kSmemFloats * 4 + kSeg * 4 * kN * static_cast<int>(sizeof(T));
 static_assert(kSmemFloats % 4 == 0, "the inputs start on 16 bytes");
 
 __device__ __forceinline__ float rd(const float *p) { return *p; }
@@ -60,74 +65,95 @@ struct WalkParams {
     float scale;
     const float *s0, *dsT;
     float *ds0;
-    float *ckpt;        // [checkpoints][H][64][64]
+    const float *ckpt, *dckpt;  // the state before each segment, D after it: [segments][H][64][64]
     float *dq_h, *dk_h; // [B,T,H,64] shares of the value heads, or null (no shared key heads)
-    int64_t nckpt;
+    int64_t nseg;       // segments of the call, the most there can be
     int *status;
 };
 
-// Checkpoint index of a sequence's first segment: sequences take disjoint runs, since each
-// needs at most one more than its share of the tokens.
-__device__ __forceinline__ int64_t first_segment(int64_t first, int64_t seq) { return first / kSeg + seq; }
+// The segment with number id: its place in its sequence (returned, -1 if none has the number) and the
+// sequence.
+__device__ __forceinline__ int64_t segment_of(const WalkParams &p, int64_t id, int64_t *seq, int64_t *first, int64_t *len)
+{
+    int64_t i = 0;
+    if (p.offsets) {
+        int64_t hi = p.nseq;  // last sequence whose run starts at or before id
+        while (hi - i > 1) {
+            const int64_t mid = (i + hi) / 2, at = min(max(static_cast<int64_t>(p.offsets[mid]), static_cast<int64_t>(0)), p.T);
+            if (at / kSeg + mid <= id) i = mid;
+            else hi = mid;
+        }
+    } else {
+        i = id / delta_first_segment(false, 1, 0, p.T);
+    }
+    *seq = i;
+    sequence_span(p.offsets, i, p.T, first, len);
+    const int64_t sg = id - delta_first_segment(p.offsets != nullptr, i, *first, p.T);
+    return sg == 0 || (sg > 0 && sg * kSeg < *len) ? sg : -1;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                   const T *__restrict__ g, const T *__restrict__ beta, const T *__restrict__ dout,
-                   T *__restrict__ dq, T *__restrict__ dk, T *__restrict__ dv, T *__restrict__ dg,
-                   T *__restrict__ dbeta)
+delta_segments_kernel(const WalkParams p, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                      const T *__restrict__ g, const T *__restrict__ beta, const T *__restrict__ dout,
+                      T *__restrict__ dq, T *__restrict__ dk, T *__restrict__ dv, T *__restrict__ dg,
+                      T *__restrict__ dbeta)
 {
     extern __shared__ float sm[];
-    float *states = sm, *rs = sm + kSeg * 4096, *part = rs + kSeg * kN, *scalars = part + kSeg * 8 * kPart;
+    float *states = sm, *rs = sm + kStates, *part = rs + kSeg * kN, *scalars = part + kSeg * 8 * kPart;
     T *inputs = reinterpret_cast<T *>(sm + kSmemFloats);
-    const int64_t n = blockIdx.x, seq = n / p.H, h = n % p.H, hk = h / (p.H / p.Hk);
+    const int64_t id = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
+    int64_t seq, first, len;
+    const int64_t sg = segment_of(p, id, &seq, &first, &len);
+    if (sg < 0) return;  // a number that no segment has
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = lane >> 2, row = 8 * rg;
     const int col = 8 * warp + 2 * (lane & 3);
-    int64_t first, len;
-    sequence_span(p.offsets, seq, p.T, &first, &len);
-    const int64_t nseg = (len + kSeg - 1) / kSeg, seg0 = first_segment(first, seq);
-    const int64_t ntok = p.B * p.T;
-    if (!in_bounds(p.status, first, len, ntok) || !in_bounds(p.status, seg0, nseg, p.nckpt)) return;
+    const int64_t ntok = p.B * p.T, t0 = first + sg * kSeg;
+    const int cnt = static_cast<int>(min(static_cast<int64_t>(kSeg), len - sg * kSeg));
+    const bool alone = len <= kSeg;  // its sequence's only segment
+    if (!in_bounds(p.status, t0, cnt, ntok) || !in_bounds(p.status, id, 1, p.nseg)) return;
 
-    float S[8][2], D[8][2];
-    const int64_t base = (seq * p.H + h) * kN * kN;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        const float2 x = p.s0 ? *reinterpret_cast<const float2 *>(p.s0 + base + (row + m) * kN + col) : make_float2(0.f, 0.f);
-        S[m][0] = x.x, S[m][1] = x.y;
-    }
-    // A segment's inputs, copied ahead (of the first pass over it, k and v alone); thread i < 16
-    // brings g or beta of one token, through a register.
-    float sc = 0.f;
-    auto stage = [&](int64_t sg, bool all) {
+    // ---- the segment's inputs to shared memory; thread i < 16 brings g or beta of one token
+    {
         constexpr int kE = 16 / static_cast<int>(sizeof(T)), kQ = kN / kE;
-        const int per = (all ? 4 : 2) * kQ;
-        for (int i = tid; i < kSeg * per; i += kThreads) {
-            const int x = i / per, arr = i % per / kQ, c = i % kQ * kE;
-            const int64_t t = first + sg * kSeg + x;
-            if (sg * kSeg + x >= len) break;
+        for (int i = tid; i < cnt * 4 * kQ; i += kThreads) {
+            const int x = i / (4 * kQ), arr = i % (4 * kQ) / kQ, c = i % kQ * kE;
             const T *src = arr == 0 ? k : arr == 1 ? v : arr == 2 ? q : dout;
-            src += (t * (arr == 0 || arr == 2 ? p.Hk : p.H) + (arr == 0 || arr == 2 ? hk : h)) * kN + c;
-            T *dst = inputs + (((sg & 1) * kSeg + x) * 4 + arr) * kN + c;
+            src += ((t0 + x) * (arr == 0 || arr == 2 ? p.Hk : p.H) + (arr == 0 || arr == 2 ? hk : h)) * kN + c;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                             static_cast<uint32_t>(__cvta_generic_to_shared(inputs + (x * 4 + arr) * kN + c))),
                          "l"(src)
                          : "memory");
         }
-        if (tid < 2 * kSeg && sg * kSeg + tid / 2 < len)
-            sc = rd((tid & 1 ? beta : g) + (first + sg * kSeg + tid / 2) * p.H + h);
-    };
-    auto arrived = [&](int64_t sg) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (tid < 2 * kSeg) scalars[(sg & 1) * 2 * kSeg + tid] = tid & 1 ? sc : expf(sc);
-        __syncthreads();
-    };
-    // one token forward: S becomes the state after it; r (this lane's two columns) is returned
-    auto step = [&](int64_t sg, int i, float (&r)[2]) {
-        const T *in = inputs + ((sg & 1) * kSeg + i) * 4 * kN;
-        const float *ab = scalars + ((sg & 1) * kSeg + i) * 2;
-        const float a = ab[0], b = ab[1];
-        float kk[8], ks[2] = {};
+        if (tid < 2 * cnt) {
+            const float x = rd((tid & 1 ? beta : g) + (t0 + tid / 2) * p.H + h);
+            scalars[tid] = tid & 1 ? x : expf(x);
+        }
+    }
+    float S[8][2], D[8][2];
+    const int64_t base = (seq * p.H + h) * kN * kN, ck = (id * p.H + h) * kN * kN;
+    const float *s_in = sg == 0 ? (p.s0 ? p.s0 + base : nullptr) : p.ckpt + ck;
+    const float *d_in = alone ? (p.dsT ? p.dsT + base : nullptr) : p.dckpt + ck;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const int64_t at = (row + m) * kN + col;
+        const float2 x = s_in ? *reinterpret_cast<const float2 *>(s_in + at) : make_float2(0.f, 0.f);
+        const float2 y = d_in ? *reinterpret_cast<const float2 *>(d_in + at) : make_float2(0.f, 0.f);
+        S[m][0] = x.x, S[m][1] = x.y, D[m][0] = y.x, D[m][1] = y.y;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // ---- forward: the state before each token, r
+    for (int i = 0; i < cnt; ++i) {
+        if (i % kKeep == 0) {
+            float4 *mine = reinterpret_cast<float4 *>(states) + i / kKeep * 1024 + tid;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                mine[m * 256] = make_float4(S[2 * m][0], S[2 * m][1], S[2 * m + 1][0], S[2 * m + 1][1]);
+        }
+        const T *in = inputs + i * 4 * kN;
+        const float a = scalars[2 * i], b = scalars[2 * i + 1];
+        float kk[8], ks[2] = {}, r[2];
         rd8(in + row, kk);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
@@ -146,123 +172,99 @@ delta_walks_kernel(const WalkParams p, const T *__restrict__ q, const T *__restr
             S[m][0] = fmaf(kk[m], b * r[0], a * S[m][0]);
             S[m][1] = fmaf(kk[m], b * r[1], a * S[m][1]);
         }
-    };
-    float r[2];
-    if (nseg > 0) stage(0, nseg == 1);
-    for (int64_t sg = 0; sg < nseg; ++sg) {
-        arrived(sg);  // and the segment before has been read
-        if (sg + 1 < nseg) stage(sg + 1, sg + 2 == nseg);
-        float *ck = p.ckpt + ((seg0 + sg) * p.H + h) * kN * kN;
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-            *reinterpret_cast<float2 *>(ck + (row + m) * kN + col) = make_float2(S[m][0], S[m][1]);
-        if (sg + 1 < nseg)
-            for (int i = 0; i < kSeg; ++i) step(sg, i, r);
+        if (rg == 0) *reinterpret_cast<float2 *>(rs + i * kN + col) = make_float2(r[0], r[1]);
     }
+    __syncwarp();
+    // ---- and back
+    for (int i = cnt - 1; i >= 0; --i) {
+        const int64_t th = (t0 + i) * p.H + h;
+        const float4 *mine = reinterpret_cast<const float4 *>(states) + i / kKeep * 1024 + tid;
+        const T *in = inputs + i * 4 * kN;
+        const float a = scalars[2 * i], b = scalars[2 * i + 1], d0 = rd(in + 3 * kN + col), d1 = rd(in + 3 * kN + col + 1);
+        const float2 rr = *reinterpret_cast<const float2 *>(rs + i * kN + col);
+        float kk[8], qq[8], pdq[8], sp[8][2], du[2] = {};
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        const float2 x = p.dsT ? *reinterpret_cast<const float2 *>(p.dsT + base + (row + m) * kN + col) : make_float2(0.f, 0.f);
-        D[m][0] = x.x, D[m][1] = x.y;
-    }
-    for (int64_t sg = nseg - 1; sg >= 0; --sg) {
-        const int64_t t0 = first + sg * kSeg;
-        const int cnt = static_cast<int>(min(static_cast<int64_t>(kSeg), len - sg * kSeg));
-        const float *ck = p.ckpt + ((seg0 + sg) * p.H + h) * kN * kN;
-        if (sg + 1 < nseg) arrived(sg);
-        if (sg > 0) stage(sg - 1, true);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {  // this thread's own elements, written above
-            const float2 x = *reinterpret_cast<const float2 *>(ck + (row + m) * kN + col);
-            S[m][0] = x.x, S[m][1] = x.y;
+        for (int m = 0; m < 4; ++m) {
+            const float4 x = mine[m * 256];
+            sp[2 * m][0] = x.x, sp[2 * m][1] = x.y, sp[2 * m + 1][0] = x.z, sp[2 * m + 1][1] = x.w;
         }
-        for (int i = 0; i < cnt; ++i) {
-            float4 *mine = reinterpret_cast<float4 *>(states) + i * 1024 + tid;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) mine[m * 256] = make_float4(S[2 * m][0], S[2 * m][1], S[2 * m + 1][0], S[2 * m + 1][1]);
-            step(sg, i, r);
-            if (rg == 0) *reinterpret_cast<float2 *>(rs + i * kN + col) = make_float2(r[0], r[1]);
-        }
-        __syncwarp();
-        for (int i = cnt - 1; i >= 0; --i) {
-            const int64_t th = (t0 + i) * p.H + h;
-            const float4 *mine = reinterpret_cast<const float4 *>(states) + i * 1024 + tid;
-            const T *in = inputs + ((sg & 1) * kSeg + i) * 4 * kN;
-            const float *ab = scalars + ((sg & 1) * kSeg + i) * 2;
-            const float a = ab[0], b = ab[1], d0 = rd(in + 3 * kN + col), d1 = rd(in + 3 * kN + col + 1);
-            const float2 rr = *reinterpret_cast<const float2 *>(rs + i * kN + col);
-            float kk[8], qq[8], pdq[8], sp[8][2], du[2] = {};
-            rd8(in + row, kk);
-            rd8(in + 2 * kN + row, qq);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float4 x = mine[m * 256];
-                sp[2 * m][0] = a * x.x, sp[2 * m][1] = a * x.y, sp[2 * m + 1][0] = a * x.z, sp[2 * m + 1][1] = a * x.w;
-            }
+        for (int j = i / kKeep * kKeep; j < i; ++j) {  // the state before token i
+            const float aj = scalars[2 * j], bj = scalars[2 * j + 1];
+            const float2 rj = *reinterpret_cast<const float2 *>(rs + j * kN + col);
+            rd8(inputs + j * 4 * kN + row, kk);
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
-                D[m][0] = fmaf(p.scale * qq[m], d0, D[m][0]);
-                D[m][1] = fmaf(p.scale * qq[m], d1, D[m][1]);
-                du[0] = fmaf(kk[m], D[m][0], du[0]);
-                du[1] = fmaf(kk[m], D[m][1], du[1]);
-                pdq[m] = p.scale * (fmaf(kk[m], b * rr.x, sp[m][0]) * d0 + fmaf(kk[m], b * rr.y, sp[m][1]) * d1);
+                sp[m][0] = fmaf(kk[m], bj * rj.x, aj * sp[m][0]);
+                sp[m][1] = fmaf(kk[m], bj * rj.y, aj * sp[m][1]);
             }
+        }
 #pragma unroll
-            for (int d = 4; d < 32; d *= 2) {
-                du[0] += __shfl_xor_sync(0xffffffffu, du[0], d);
-                du[1] += __shfl_xor_sync(0xffffffffu, du[1], d);
-            }
-            const float v0 = b * du[0], v1 = b * du[1];
-            float pdb = rg == 0 ? du[0] * rr.x + du[1] * rr.y : 0.f, pdg = 0.f, pdk[8];
+        for (int m = 0; m < 8; ++m) sp[m][0] *= a, sp[m][1] *= a;
+        rd8(in + row, kk);
+        rd8(in + 2 * kN + row, qq);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            D[m][0] = fmaf(p.scale * qq[m], d0, D[m][0]);
+            D[m][1] = fmaf(p.scale * qq[m], d1, D[m][1]);
+            du[0] = fmaf(kk[m], D[m][0], du[0]);
+            du[1] = fmaf(kk[m], D[m][1], du[1]);
+            pdq[m] = p.scale * (fmaf(kk[m], b * rr.x, sp[m][0]) * d0 + fmaf(kk[m], b * rr.y, sp[m][1]) * d1);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) {
+            du[0] += __shfl_xor_sync(0xffffffffu, du[0], d);
+            du[1] += __shfl_xor_sync(0xffffffffu, du[1], d);
+        }
+        const float v0 = b * du[0], v1 = b * du[1];
+        float pdb = rg == 0 ? du[0] * rr.x + du[1] * rr.y : 0.f, pdg = 0.f, pdk[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            pdk[m] = D[m][0] * (b * rr.x) + D[m][1] * (b * rr.y) - sp[m][0] * v0 - sp[m][1] * v1;
+            const float e0 = fmaf(-kk[m], v0, D[m][0]), e1 = fmaf(-kk[m], v1, D[m][1]);
+            pdg = fmaf(e0, sp[m][0], fmaf(e1, sp[m][1], pdg));
+            D[m][0] = a * e0;
+            D[m][1] = a * e1;
+        }
+#pragma unroll
+        for (int d = 1; d < 4; d *= 2)
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
-                pdk[m] = D[m][0] * (b * rr.x) + D[m][1] * (b * rr.y) - sp[m][0] * v0 - sp[m][1] * v1;
-                const float e0 = fmaf(-kk[m], v0, D[m][0]), e1 = fmaf(-kk[m], v1, D[m][1]);
-                pdg = fmaf(e0, sp[m][0], fmaf(e1, sp[m][1], pdg));
-                D[m][0] = a * e0;
-                D[m][1] = a * e1;
+                pdq[m] += __shfl_xor_sync(0xffffffffu, pdq[m], d);
+                pdk[m] += __shfl_xor_sync(0xffffffffu, pdk[m], d);
             }
 #pragma unroll
-            for (int d = 1; d < 4; d *= 2)
+        for (int d = 1; d < 32; d *= 2) {
+            pdb += __shfl_xor_sync(0xffffffffu, pdb, d);
+            pdg += __shfl_xor_sync(0xffffffffu, pdg, d);
+        }
+        float *pp = part + (i * 8 + warp) * kPart;
+        if ((lane & 3) == 0) {
 #pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    pdq[m] += __shfl_xor_sync(0xffffffffu, pdq[m], d);
-                    pdk[m] += __shfl_xor_sync(0xffffffffu, pdk[m], d);
-                }
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                pdb += __shfl_xor_sync(0xffffffffu, pdb, d);
-                pdg += __shfl_xor_sync(0xffffffffu, pdg, d);
-            }
-            float *pp = part + (i * 8 + warp) * kPart;
-            if ((lane & 3) == 0) {
-#pragma unroll
-                for (int m = 0; m < 8; ++m) {
-                    pp[row + m] = pdq[m];
-                    pp[kN + row + m] = pdk[m];
-                }
-            }
-            if (lane == 0) {
-                pp[2 * kN] = pdb;
-                pp[2 * kN + 1] = pdg;
-            }
-            if (rg == 0) {
-                wr(dv + th * kN + col, v0);
-                wr(dv + th * kN + col + 1, v1);
+            for (int m = 0; m < 8; ++m) {
+                pp[row + m] = pdq[m];
+                pp[kN + row + m] = pdk[m];
             }
         }
-        __syncthreads();
-        for (int e = tid; e < cnt * kPart; e += kThreads) {
-            const int i = e / kPart, x = e % kPart;
-            float sum = 0.f;
-            for (int w = 0; w < 8; ++w) sum += part[(i * 8 + w) * kPart + x];
-            const int64_t t = t0 + i, th = t * p.H + h;
-            if (x >= 2 * kN) wr((x == 2 * kN ? dbeta : dg) + th, sum);
-            else if (p.dq_h) (x < kN ? p.dq_h : p.dk_h)[th * kN + (x & (kN - 1))] = sum;
-            else wr((x < kN ? dq : dk) + th * kN + (x & (kN - 1)), sum);
+        if (lane == 0) {
+            pp[2 * kN] = pdb;
+            pp[2 * kN + 1] = pdg;
         }
-        __syncthreads();
+        if (rg == 0) {
+            wr(dv + th * kN + col, v0);
+            wr(dv + th * kN + col + 1, v1);
+        }
     }
-    if (p.ds0) {
+    __syncthreads();
+    for (int e = tid; e < cnt * kPart; e += kThreads) {
+        const int i = e / kPart, x = e % kPart;
+        float sum = 0.f;
+        for (int w = 0; w < 8; ++w) sum += part[(i * 8 + w) * kPart + x];
+        const int64_t t = t0 + i, th = t * p.H + h;
+        if (x >= 2 * kN) wr((x == 2 * kN ? dbeta : dg) + th, sum);
+        else if (p.dq_h) (x < kN ? p.dq_h : p.dk_h)[th * kN + (x & (kN - 1))] = sum;
+        else wr((x < kN ? dq : dk) + th * kN + (x & (kN - 1)), sum);
+    }
+    if (p.ds0 && sg == 0) {
 #pragma unroll
         for (int m = 0; m < 8; ++m)
             *reinterpret_cast<float2 *>(p.ds0 + base + (row + m) * kN + col) = make_float2(D[m][0], D[m][1]);
@@ -300,10 +302,11 @@ delta_sum_heads_kernel(int64_t ntok, int64_t Hk, int64_t H, int64_t nseq, const 
     wr(dk + e, b);
 }
 
-int64_t checkpoints(const DeltaArgs &a)
-{
-    return a.offsets ? a.T / kSeg + a.nseq : a.B * ((a.T + kSeg - 1) / kSeg + 1);
-}
+// Numbers of segments in use and unused: where those of one more sequence would start.
+int64_t segments(const DeltaArgs &a) { return delta_first_segment(a.offsets != nullptr, a.nseq, a.B * a.T, a.T); }
+// Whether every sequence is known to be of one segment: no walks, no checkpoints.
+bool single(const DeltaArgs &a) { return !a.offsets && a.T <= kSeg; }
+int64_t checkpoint_floats(const DeltaArgs &a) { return single(a) ? 0 : segments(a) * a.H * kN * kN; }
 
 template <typename T> cudaError_t launch(const DeltaBwdArgs &a, cudaStream_t s)
 {
@@ -314,16 +317,21 @@ template <typename T> cudaError_t launch(const DeltaBwdArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev]) {  // racing first calls set the same attribute: harmless
-        e = cudaFuncSetAttribute(delta_walks_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<T>);
+        e = cudaFuncSetAttribute(delta_segments_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<T>);
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
-    const int64_t ntok = f.B * f.T, nck = checkpoints(f);
-    float *ck = static_cast<float *>(a.workspace);
-    float *share = f.H == f.Hk ? nullptr : ck + nck * f.H * kN * kN;
-    const WalkParams p{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, f.scale, f.s0, a.dsT, a.ds0, ck,
-                       share, share ? share + ntok * f.H * kN : nullptr, nck, f.status};
-    delta_walks_kernel<T><<<static_cast<unsigned>(f.nseq * f.H), kThreads, kSmemBytes<T>, s>>>(
+    const int64_t ntok = f.B * f.T, nseg = segments(f), nck = checkpoint_floats(f);
+    if (nseg * f.H > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    float *ck = static_cast<float *>(a.workspace), *dck = ck + nck;
+    float *share = f.H == f.Hk ? nullptr : dck + nck;
+    if (!single(f)) {
+        e = delta_checkpoints_launch(a, ck, dck, s);
+        if (e != cudaSuccess) return e;
+    }
+    const WalkParams p{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, f.scale, f.s0, a.dsT, a.ds0, ck, dck,
+                       share, share ? share + ntok * f.H * kN : nullptr, nseg, f.status};
+    delta_segments_kernel<T><<<static_cast<unsigned>(nseg * f.H), kThreads, kSmemBytes<T>, s>>>(
         p, static_cast<const T *>(f.q), static_cast<const T *>(f.k), static_cast<const T *>(f.v),
         static_cast<const T *>(f.g), static_cast<const T *>(f.beta), static_cast<const T *>(a.dout),
         static_cast<T *>(a.dq), static_cast<T *>(a.dk), static_cast<T *>(a.dv), static_cast<T *>(a.dg),
@@ -354,7 +362,7 @@ cudaError_t delta_sum_heads_launch(const DeltaBwdArgs &a, const float *dq_h, con
 size_t delta_walks_workspace_bytes(const DeltaArgs &a)
 {
     const int64_t shares = a.H == a.Hk ? 0 : 2 * a.B * a.T * a.H * kN;
-    return static_cast<size_t>(checkpoints(a) * a.H * kN * kN + shares) * sizeof(float);
+    return static_cast<size_t>(2 * checkpoint_floats(a) + shares) * sizeof(float);
 }
 
 cudaError_t delta_backward_walks_launch(const DeltaBwdArgs &a, cudaStream_t s)

@@ -244,13 +244,20 @@ template <int COLS> struct WalkToken {
     float v[COLS], a, b;
 };
 
-template <typename T, int COLS>
+// What a walk is for.  kStates: the state before every segment of the backward pass (q and o unused).
+// kGradients: the walk back for the gradient D of the state (v: the outputs' gradients, s0: the last
+// state's), D after every segment:
+//   D += scale q_t^T do_t,   du = k_t D,   D = exp(g_t) (D - beta_t k_t^T du)
+enum { kOutputs, kStates, kGradients };
+
+template <typename T, int COLS, int MODE>
 __global__ void __launch_bounds__(kThreads)
 delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, const int32_t *__restrict__ offsets,
                   int64_t nslots, const int32_t *__restrict__ slots, const T *__restrict__ q, const T *__restrict__ k,
                   const T *__restrict__ v, const T *__restrict__ g, const T *__restrict__ beta, float scale,
-                  const float *s0, T *__restrict__ o, float *sT, int *status)
+                  const float *s0, T *__restrict__ o, float *sT, float *ckpt, int64_t nckpt, int *status)
 {
+    if (MODE == kStates) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the other walk
     constexpr int kParts = 2 / COLS;  // blocks of a (sequence, head)
     const int64_t n = blockIdx.x / kParts, seq = n / H, h = n % H, hk = h / (H / Hk);
     const int lane = threadIdx.x & 31, rg = lane >> 3, warp = threadIdx.x >> 5;
@@ -258,10 +265,15 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
     const int col = col0 + COLS * (lane & 7);
     int64_t first, len64;
     sequence_span(offsets, seq, Tn, &first, &len64);
-    const int len = in_bounds(status, first, len64, B * Tn) ? static_cast<int>(len64) : 0;
+    const int tokens = in_bounds(status, first, len64, B * Tn) ? static_cast<int>(len64) : 0;
+    const int nseg = (tokens + kDeltaSeg - 1) / kDeltaSeg;
+    // tokens to walk; the i-th of them is token_at(i)
+    const int len = MODE == kOutputs ? tokens : nseg < 2 ? 0 : MODE == kStates ? (nseg - 1) * kDeltaSeg : tokens - kDeltaSeg;
+    auto token_at = [&](int i) { return MODE == kGradients ? tokens - 1 - i : i; };
     const int64_t slot = sequence_slot(slots, seq, nslots, status);
-    const int64_t at = ((slot * H + h) * kN + 4 * rg) * kN + col;  // this lane's first state element
-    const bool has = slot >= 0 && in_bounds(status, (slot * H + h) * kN * kN, kN * kN, nslots * H * kN * kN);
+    const int64_t at = 4 * rg * kN + col;  // this lane's first element of a state
+    const int64_t state = (slot * H + h) * kN * kN;
+    const bool has = slot >= 0 && in_bounds(status, state, kN * kN, nslots * H * kN * kN);
 
     __shared__ __align__(16) T ring[kThreads / 32][kRing][kRow<COLS>];
     // Copies: chunks of 16 bytes; q and k of kTok tokens at a time, a chunk a lane, then v.
@@ -273,10 +285,11 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
 #pragma unroll
         for (int x = 0; x < kGroup; x += kTok) {
             const int t = t0 + x + xq;
-            if (t < len) copy16(&ring[warp][t % kRing][cq * kE], pq + t * (Hk * kN));
+            if (t < len && (MODE != kStates || cq >= kQ))
+                copy16(&ring[warp][t % kRing][cq * kE], pq + token_at(t) * (Hk * kN));
         }
         if (xv < kGroup && t0 + xv < len)
-            copy16(&ring[warp][(t0 + xv) % kRing][2 * kN + (lane % kV) * kE], pv + (t0 + xv) * (H * kN));
+            copy16(&ring[warp][(t0 + xv) % kRing][2 * kN + (lane % kV) * kE], pv + token_at(t0 + xv) * (H * kN));
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // At most kGroups - 2 groups are under way after this.
@@ -289,12 +302,12 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
     float ac = 0.f, bc = 0.f, gn = 0.f, bn = 0.f;
     auto scalars = [&](int t) {
         const bool in = t + lane < len;
-        gn = in ? ld1(gh + (t + lane) * H) : 0.f;
-        bn = in ? ld1(bh + (t + lane) * H) : 0.f;
+        gn = in ? ld1(gh + token_at(t + lane) * H) : 0.f;
+        bn = in ? ld1(bh + token_at(t + lane) * H) : 0.f;
     };
     auto load = [&](int t, WalkToken<COLS> &x) {  // t = 0, 1, ... in turn, its group complete
         const T *row = ring[warp][t % kRing];
-        ld_rows(row, rg, x.q);
+        if (MODE != kStates) ld_rows(row, rg, x.q);
         ld_rows(row + kN, rg, x.k);
         ldc(row + 2 * kN + COLS * (lane & 7), x.v);
         if (t % 32 == 0) {
@@ -313,15 +326,62 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
     for (int m = 0; m < 8; ++m) {
         float x[COLS] = {}, y[COLS] = {};
         if (s0 && has) {
-            const float *p = s0 + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
+            const float *p = s0 + state + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
             ldc(p, x);
             ldc(p + kN, y);
         }
 #pragma unroll
         for (int c = 0; c < COLS; ++c) S[c][m] = pack2(x[c], y[c]);
     }
-    T *po = o + (first * H + h) * kN + col;
+    auto put = [&](float *p0) {  // the state to memory
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            float *p = p0 + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
+            float x[COLS], y[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) asm("mov.b64 {%0, %1}, %2;" : "=f"(x[c]), "=f"(y[c]) : "l"(S[c][m]));
+            stc(p, x);
+            stc(p + kN, y);
+        }
+    };
+    auto checkpoint = [&](int sg) {
+        const int64_t id = delta_first_segment(offsets != nullptr, seq, first, Tn) + sg;
+        if (in_bounds(status, id, 1, nckpt)) put(ckpt + (id * H + h) * kN * kN);
+    };
+    if (MODE == kGradients && nseg > 1) checkpoint(nseg - 1);
+    T *po = MODE == kOutputs ? o + (first * H + h) * kN + col : nullptr;
     auto step = [&](int t, const WalkToken<COLS> &x) {
+        if constexpr (MODE == kGradients) {
+            uint64_t du2[COLS] = {};
+            float du[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                const float d = scale * x.v[c];
+                const uint64_t d2 = pack2(d, d);
+#pragma unroll
+                for (int m = 0; m < 8; ++m) S[c][m] = fma2(x.q[m], d2, S[c][m]);
+            }
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) du2[c] = fma2(x.k[m], S[c][m], du2[c]);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) du[c] = sum2(du2[c]);
+#pragma unroll
+            for (int d = 8; d < 32; d *= 2)
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) du[c] += __shfl_xor_sync(0xffffffffu, du[c], d);
+            const uint64_t a2 = pack2(x.a, x.a);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                const uint64_t w2 = pack2(-x.b * du[c], -x.b * du[c]);
+#pragma unroll
+                for (int m = 0; m < 8; ++m) S[c][m] = mul2(a2, fma2(x.k[m], w2, S[c][m]));
+            }
+            const int token = token_at(t);
+            if (token % kDeltaSeg == 0) checkpoint(token / kDeltaSeg - 1);
+            return;
+        }
         uint64_t ks[COLS] = {}, qs[COLS] = {}, qk2 = 0;
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
@@ -333,6 +393,7 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
         for (int c = 0; c < COLS; ++c) r[c] = sum2(ks[c]);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
+            if (MODE == kStates) break;
             qk2 = fma2(x.q[m], x.k[m], qk2);
 #pragma unroll
             for (int c = 0; c < COLS; ++c) qs[c] = fma2(x.q[m], S[c][m], qs[c]);
@@ -349,6 +410,7 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
         for (int d = 8; d < 32; d *= 2) {
 #pragma unroll
             for (int c = 0; c < COLS; ++c) r[c] += __shfl_xor_sync(0xffffffffu, r[c], d);
+            if (MODE == kStates) continue;
             qk += __shfl_xor_sync(0xffffffffu, qk, d);
 #pragma unroll
             for (int c = 0; c < COLS; ++c) w[c] += __shfl_xor_sync(0xffffffffu, w[c], d);
@@ -362,7 +424,8 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
             for (int m = 0; m < 8; ++m) S[c][m] = fma2(x.k[m], u2, S[c][m]);
             out[c] = scale * fmaf(qk, u, x.a * w[c]);
         }
-        if (rg == 0) stc(po + t * (H * kN), out);
+        if (MODE == kOutputs && rg == 0) stc(po + t * (H * kN), out);
+        if (MODE == kStates && t % kDeltaSeg == kDeltaSeg - 1) checkpoint(t / kDeltaSeg + 1);
     };
     WalkToken<COLS> x, y;
     arrived();  // group 0
@@ -381,17 +444,8 @@ delta_walk_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nseq, co
             step(t + i + 1, y);
         }
     }
-    if (sT && has) {
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            float *p = sT + at + (16 * (m / 2) + 2 * (m % 2)) * kN;
-            float x[COLS], y[COLS];
-#pragma unroll
-            for (int c = 0; c < COLS; ++c) asm("mov.b64 {%0, %1}, %2;" : "=f"(x[c]), "=f"(y[c]) : "l"(S[c][m]));
-            stc(p, x);
-            stc(p + kN, y);
-        }
-    }
+    if (MODE == kOutputs && sT && has) put(sT + state);
+    if (MODE == kGradients) asm volatile("griddepcontrol.wait;" ::: "memory");  // see the launch
 }
 
 // Shortest mean sequence that takes the second kernel.  First against second, bf16, us (B1 H4, B64
@@ -409,15 +463,58 @@ template <typename T> cudaError_t launch(const DeltaArgs &a, cudaStream_t s)
 {
     const int64_t pairs = a.nseq * a.H;
     const bool walk = (a.offsets ? a.T / a.nseq : a.T) >= kWalkTokens, narrow = walk && pairs <= kNarrowPairs;
-    const auto kernel = narrow ? delta_walk_kernel<T, 1> : walk ? delta_walk_kernel<T, 2> : delta_recurrent_kernel<T>;
+    if (!walk) {
+        delta_recurrent_kernel<T><<<static_cast<unsigned>(pairs), kThreads, 0, s>>>(
+            a.B, a.T, a.Hk, a.H, a.nseq, a.offsets, a.nslots, a.slots, static_cast<const T *>(a.q),
+            static_cast<const T *>(a.k), static_cast<const T *>(a.v), static_cast<const T *>(a.g),
+            static_cast<const T *>(a.beta), a.scale, a.s0, static_cast<T *>(a.o), a.sT, a.status);
+        return cudaGetLastError();
+    }
+    const auto kernel = narrow ? delta_walk_kernel<T, 1, kOutputs> : delta_walk_kernel<T, 2, kOutputs>;
     kernel<<<static_cast<unsigned>(narrow ? 2 * pairs : pairs), kThreads, 0, s>>>(
         a.B, a.T, a.Hk, a.H, a.nseq, a.offsets, a.nslots, a.slots, static_cast<const T *>(a.q),
         static_cast<const T *>(a.k), static_cast<const T *>(a.v), static_cast<const T *>(a.g),
-        static_cast<const T *>(a.beta), a.scale, a.s0, static_cast<T *>(a.o), a.sT, a.status);
+        static_cast<const T *>(a.beta), a.scale, a.s0, static_cast<T *>(a.o), a.sT, nullptr, 0, a.status);
     return cudaGetLastError();
 }
 
+template <typename T> cudaError_t launch_checkpoints(const DeltaBwdArgs &b, float *states, float *grads, cudaStream_t s)
+{
+    const DeltaArgs &a = b.f;
+    const int64_t pairs = a.nseq * a.H, ntok = a.B * a.T;
+    const int64_t nckpt = delta_first_segment(a.offsets != nullptr, a.nseq, ntok, a.T);  // where one more would start
+    const bool narrow = 2 * pairs <= kNarrowPairs;  // two grids at a time
+    const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v);
+    const T *g = static_cast<const T *>(a.g), *beta = static_cast<const T *>(a.beta);
+    const unsigned grid = static_cast<unsigned>(narrow ? 2 * pairs : pairs);
+    (narrow ? delta_walk_kernel<T, 1, kStates> : delta_walk_kernel<T, 2, kStates>)<<<grid, kThreads, 0, s>>>(
+        a.B, a.T, a.Hk, a.H, a.nseq, a.offsets, a.nseq, nullptr, q, k, v, g, beta, a.scale, a.s0, nullptr, nullptr, states,
+        nckpt, a.status);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // The walk back needs nothing of the other and may start beside it (a programmatic launch); it ends
+    // only after the other has, so that the next kernel, launched as usual, follows both.
+    cudaLaunchAttribute beside[1];
+    beside[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    beside[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = beside;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, narrow ? delta_walk_kernel<T, 1, kGradients> : delta_walk_kernel<T, 2, kGradients>, a.B,
+                              a.T, a.Hk, a.H, a.nseq, a.offsets, a.nseq, static_cast<const int32_t *>(nullptr), q, k,
+                              static_cast<const T *>(b.dout), g, beta, a.scale, b.dsT, static_cast<T *>(nullptr),
+                              static_cast<float *>(nullptr), grads, nckpt, a.status);
+}
+
 }  // namespace
+
+cudaError_t delta_checkpoints_launch(const DeltaBwdArgs &a, float *states, float *grads, cudaStream_t s)
+{
+    return a.f.bf16 ? launch_checkpoints<__nv_bfloat16>(a, states, grads, s) : launch_checkpoints<float>(a, states, grads, s);
+}
 
 cudaError_t delta_recurrent_launch(const DeltaArgs &a, cudaStream_t s)
 {

@@ -356,8 +356,8 @@ int delta_sizes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int64_t 
 // Shortest mean sequences of bf16 that take the tensor cores; shorter ones and fp32 are walked
 // token by token.  A chunk costs the same however few tokens it holds, a walk grows with them.
 // Forward, walk against chunked, us (B1 H4, B8 H32, B64 H32): 20 tokens 10 / 12, 16 / 16, 66 / 72; 28
-// tokens 12 / 12, 20 / 18, 86 / 74.  Backward: 8 tokens 14 / 25, 27 / 37, 156 / 166; 10 tokens 20 / 26,
-// 39 / 35, 233 / 166 (the walks' segments are of 8).
+// tokens 12 / 12, 20 / 18, 86 / 74.  Backward: 8 tokens 16 / 24, 22 / 37, 106 / 164; 9 tokens 20 / 25,
+// 39 / 35, 174 / 164 (beyond one segment of 8 two walks come first).
 constexpr int64_t kDeltaChunkedTokens = 24, kDeltaBwdChunkedTokens = 9;
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }

@@ -202,6 +202,16 @@ struct DeltaBwdArgs {
     float *ds0;                 // [nseq,H,64,64] or null
     void *workspace;
 };
+// The exact walks work on segments of 8 tokens.  The segments of a call are numbered through: sequences
+// take disjoint runs of at least one number each.
+constexpr int kDeltaSeg = 8;
+__host__ __device__ __forceinline__ int64_t delta_first_segment(bool packed, int64_t seq, int64_t first, int64_t T)
+{
+    return packed ? first / kDeltaSeg + seq : seq * (T > 0 ? (T + kDeltaSeg - 1) / kDeltaSeg : 1);
+}
+// The state before every segment but a sequence's first, and the gradient of the state after every
+// segment (of sequences of one segment: neither), fp32 [segments][H][64][64].
+cudaError_t delta_checkpoints_launch(const DeltaBwdArgs &a, float *states, float *grads, cudaStream_t s);
 size_t delta_walks_workspace_bytes(const DeltaArgs &a);
 size_t delta_backward_tc_workspace_bytes(const DeltaArgs &a);  // bf16
 cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s);
