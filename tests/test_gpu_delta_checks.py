@@ -6,6 +6,7 @@ device status word; these calls have to leave it at 0 and give the values of the
 reference (tolerances: those of test_gpu_delta.py, derived there).
 """
 import os
+import threading
 
 import pytest
 import torch
@@ -126,3 +127,55 @@ def test_most_packed_pairs():
     x = ref.inputs(1, sum(lens), 1, 2, BF16, seed=5, nseq=len(lens))
     spans = ref.spans_of(lens)
     _check_forward(x, spans, [a for a, _ in spans] + [sum(lens)])
+
+
+def test_two_threads_on_their_own_streams():
+    """Calls that overlap, each with its own workspace: the values of calls made alone."""
+    cases = [(1, 700, 2, 4, BF16), (2, 300, 1, 2, F32)]
+    xs = [_cu(ref.inputs(*c, seed=i)) for i, c in enumerate(cases)]
+
+    def run(x):
+        o, sT = ops.delta_forward(*_args(x), s0=x["s0"])
+        return [o, sT, *ops.delta_backward(*_args(x), x["do"], s0=x["s0"], dsT=x["dsT"]).values()]
+
+    alone = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i] = run(xs[i])
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_decode_and_prefill_captured_after_an_eager_call(T):
+    """A captured call of packed sequences whose offsets and slots change between replays."""
+    x = _cu(ref.inputs(1, 3 * T, 1, 2, BF16, seed=T, nseq=3))
+    offsets = torch.tensor([0, T, 2 * T, 3 * T], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
+    pool, o = x["s0"].clone(), torch.empty_like(x["v"])
+    ops.delta_forward(*_args(x), s0=pool, offsets=offsets, slots=slots, o=o)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.delta_forward(*_args(x), s0=pool, offsets=offsets, slots=slots, o=o)
+    for lens, order in (([T, T, T], [2, 0, 1]), ([2 * T, 0, T], [1, -1, 0]), ([1, 3 * T - 2, 1], [0, 1, 2])):
+        offsets.copy_(torch.tensor([sum(lens[:i]) for i in range(4)], dtype=torch.int32))
+        slots.copy_(torch.tensor(order, dtype=torch.int32))
+        pool.copy_(x["s0"])
+        graph.replay()
+        want_pool = x["s0"].clone()
+        want, _ = ops.delta_forward(*_args(x), s0=want_pool, offsets=offsets, slots=slots)
+        assert torch.equal(o, want) and torch.equal(pool, want_pool)
+    assert ops.device_status() == 0

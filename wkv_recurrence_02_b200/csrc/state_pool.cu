@@ -15,7 +15,7 @@
 // passes through registers.  One warp moves the data (each lane issues the copies of its own
 // pairs) through two stages, so one task loads while the other is stored; blocks stay
 // resident and take tasks in turn.  Measured: 64 forks of 8 states and 2 freed slots over 12 layers of
-// 32 heads 90 us, 5.2 TB/s (nine bytes in ten are written); a pool of 256 states of 64 heads, half of
+// 32 heads 88 us, 5.3 TB/s (nine bytes in ten are written); a pool of 256 states of 64 heads, half of
 // them live, compacted in 50 us, 5.3 TB/s.
 #include "tc_common.cuh"
 
@@ -31,10 +31,21 @@ constexpr int kCopySmem = 224 * 1024;      // the copy kernel's block owns an SM
 constexpr int kZeroBytes = 8 * 1024;       // zeros for freed slots, and the largest copy range
 constexpr int kCompactStage = 32 * 1024;   // two stages, three blocks per SM
 
+// Bytes of a task's range: at most `most`, a multiple of 16, so that `blocks` blocks have the same number
+// of tasks as nearly as it can be, but no less than 512 where `most` allows (shorter bulk copies waste
+// their issue).
+__host__ __device__ int64_t pick_range(int64_t layers, int64_t slot_bytes, int64_t most, int64_t blocks)
+{
+    if (most < 16) most = 16;
+    const int64_t least = most < 512 ? most : 512, per = (slot_bytes + most - 1) / most;
+    const int64_t rounds = (layers * per + blocks - 1) / blocks, even = rounds * blocks / layers;
+    const int64_t range = even > per ? (slot_bytes + even - 1) / even : most;
+    return ((range > least ? range : least) + 15) / 16 * 16 < most ? ((range > least ? range : least) + 15) / 16 * 16
+                                                                    : most / 16 * 16;
+}
+
 struct CopyParams {
     StateCopyArgs a;
-    int64_t range;          // bytes of one task's range (a multiple of 16)
-    int64_t per_layer;      // ranges per layer
     int stage;              // bytes of one of the two stages
 };
 
@@ -103,12 +114,14 @@ state_copy_kernel(const CopyParams p)
     __syncthreads();
     if (tid >= 32) return;
     const int lane = tid;
-    const int64_t tasks = p.a.layers * p.per_layer;
+    // bytes of one task's range: the stage holds one of every source, however many pairs share them
+    const int64_t range = pick_range(p.a.layers, p.a.slot_bytes, min(kZeroBytes, p.stage / max(nload, 1) / 16 * 16), gridDim.x);
+    const int64_t per_layer = (p.a.slot_bytes + range - 1) / range, tasks = p.a.layers * per_layer;
     const int64_t layer_bytes = p.a.nslots * p.a.slot_bytes;
     const int64_t pool_bytes = p.a.layers * layer_bytes;
     auto load = [&](int64_t task, int st) {
-        const int64_t layer = task / p.per_layer, off = task % p.per_layer * p.range;
-        const uint32_t w = static_cast<uint32_t>(min(p.range, p.a.slot_bytes - off));
+        const int64_t layer = task / per_layer, off = task % per_layer * range;
+        const uint32_t w = static_cast<uint32_t>(min(range, p.a.slot_bytes - off));
         const uint32_t bar = smem_u32(&bars[st]);
         if (lane == 0) bar_expect_tx(bar, w * nload);
         __syncwarp();
@@ -116,8 +129,8 @@ state_copy_kernel(const CopyParams p)
             if (from[i] == i) {
                 const int64_t at = layer * layer_bytes + src[i] * p.a.slot_bytes + off;
                 if (in_bounds(p.a.status, at, w, pool_bytes) &&
-                    in_bounds(p.a.status, pos[i] * p.range, w, p.stage))
-                    bulk_load(smem_u32(sm + st * p.stage + pos[i] * p.range), p.a.pool + at, w, bar);
+                    in_bounds(p.a.status, pos[i] * range, w, p.stage))
+                    bulk_load(smem_u32(sm + st * p.stage + pos[i] * range), p.a.pool + at, w, bar);
             }
     };
     int64_t it = 0;
@@ -136,14 +149,14 @@ state_copy_kernel(const CopyParams p)
             bar_wait(smem_u32(&bars[st ^ 1]), static_cast<uint32_t>(((it + 1) >> 1) & 1), kWaitLimit);  // the copies in flight
             break;
         }
-        const int64_t layer = task / p.per_layer, off = task % p.per_layer * p.range;
-        const uint32_t w = static_cast<uint32_t>(min(p.range, p.a.slot_bytes - off));
+        const int64_t layer = task / per_layer, off = task % per_layer * range;
+        const uint32_t w = static_cast<uint32_t>(min(range, p.a.slot_bytes - off));
         for (int i = lane; i < n; i += 32) {
             const int f = from[i];
             if (f == -2) continue;
             const int64_t at = layer * layer_bytes + dst[i] * p.a.slot_bytes + off;
             if (in_bounds(p.a.status, at, w, pool_bytes))
-                bulk_store(p.a.pool + at, smem_u32(f < 0 ? zeros : sm + st * p.stage + pos[f] * p.range), w);
+                bulk_store(p.a.pool + at, smem_u32(f < 0 ? zeros : sm + st * p.stage + pos[f] * range), w);
         }
         bulk_commit();
     }
@@ -258,28 +271,15 @@ int64_t sms()
     return n;
 }
 
-int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
-
-// Largest range of at most `most` bytes (a multiple of 16) that still gives every one of
-// `blocks` blocks a task, but no less than 512 bytes (shorter bulk copies waste their issue).
-int64_t pick_range(int64_t layers, int64_t slot_bytes, int64_t most, int64_t blocks)
-{
-    const int64_t share = round16((layers * slot_bytes + blocks - 1) / blocks);
-    return std::max<int64_t>(16, std::min(most, std::max<int64_t>(share, 512)) / 16 * 16);
-}
-
 }  // namespace
 
 cudaError_t state_copy_launch(const StateCopyArgs &a, cudaStream_t s)
 {
     const int64_t stage = (kCopySmem - 128 - kZeroBytes - 16 * a.n) / 2 / 128 * 128;
-    const int64_t most = std::min<int64_t>(kZeroBytes, stage / a.n / 16 * 16);
-    const int64_t range = pick_range(a.layers, a.slot_bytes, most, sms());
-    const int64_t per_layer = (a.slot_bytes + range - 1) / range;
     const cudaError_t e = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopySmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(std::min(a.layers * per_layer, sms()));
-    state_copy_kernel<<<grid, kThreads, kCopySmem, s>>>(CopyParams{a, range, per_layer, static_cast<int>(stage)});
+    const unsigned grid = static_cast<unsigned>(std::min(a.layers * ((a.slot_bytes + 511) / 512), sms()));
+    state_copy_kernel<<<grid, kThreads, kCopySmem, s>>>(CopyParams{a, static_cast<int>(stage)});
     return cudaGetLastError();
 }
 
