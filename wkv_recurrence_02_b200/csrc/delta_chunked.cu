@@ -14,7 +14,7 @@
 // Accuracy.  The state is an fp32 result, so every operand between S and the next S is two bf16
 // terms, hi and lo (K and V are exact): S, W, T and diag(tail) U, three products where both
 // sides are split.  What that leaves is 2^-16 of each operand.  The output is rounded to bf16,
-// and there P, U and the S of Q S are single bf16.
+// and there P, U and the S of Q S are single bf16 (with 32 columns a CTA, below, only P is).
 //
 // A product of N = 64 takes 50 cycles of the tensor core whatever M is, one of N = 128 takes 64
 // (measured): so the two terms of an operand lie side by side as one B of 128 columns, and their
@@ -35,9 +35,10 @@
 // Measured.  Bound by the latency of the chain: one CTA alone on its SM takes 4230 cycles a chunk,
 // some 700 for each of the three products (256 to 450 of them the tensor core's) and the rest the
 // conversions between registers, shared and tensor memory; two CTAs on an SM take 6230 for a chunk
-// of each.  B8 T4096 H32: 210 us (STATES 185) after 92 for T; B8 T1024 H32: 64 us, tensor pipe 32 %
-// active, DRAM 36 %, issue 33 %.  With 32 columns a CTA some 3900 cycles a chunk.  Slower: loads issued by the output group (334 us a call against
-// 309), a vote of the group after every wait, a warp that only issues.
+// of each.  B8 T4096 H32: 210 us (STATES 185) after 84 to 91 for T; B8 T1024 H32: 64 us, tensor pipe
+// 32 % active, DRAM 36 %, issue 33 %.  With 32 columns a CTA some 3900 cycles a chunk.  Slower: loads
+// issued by the output group (331 us a call against 306), a vote of the group after every wait, a
+// warp that only issues.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records RWKV_ERR_TIMEOUT in the device
 // status word, waits (bounded) for its own copies and MMAs, frees its tensor memory and returns.
