@@ -179,3 +179,40 @@ def test_decode_and_prefill_captured_after_an_eager_call(T):
         want, _ = ops.delta_forward(*_args(x), s0=want_pool, offsets=offsets, slots=slots)
         assert torch.equal(o, want) and torch.equal(pool, want_pool)
     assert ops.device_status() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """2^31 elements of v and more: the last tokens as in a call of their own, which starts from the state
+    that the tokens before leave (chunks then start at the same tokens)."""
+    T, H, n = (1 << 20) + 64, 32, 192
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF16)  # noqa: E731
+    unit = lambda x: torch.nn.functional.normalize(x.float(), dim=-1).to(BF16)  # noqa: E731
+    x = [unit(rn(1, T, 1, 64)), unit(rn(1, T, 1, 64)), rn(1, T, H, 64), -rn(1, T, H).abs(), torch.sigmoid(rn(1, T, H))]
+    assert x[2].numel() > 1 << 31
+    head, tail = [t[:, :T - n] for t in x], [t[:, T - n:] for t in x]
+    o, sT = ops.delta_forward(*x)
+    o_tail = o[:, T - n:].clone()
+    _, mid = ops.delta_forward(*head, o=o[:, :T - n])
+    o2, sT2 = ops.delta_forward(*tail, s0=mid)
+    assert torch.equal(o_tail, o2) and torch.equal(sT, sT2)
+    del o, o2, head
+    do, dsT = rn(1, T, H, 64), 0.1 * torch.randn(1, H, 64, 64, generator=gen, device="cuda")
+    got = {m: t[:, T - n:].clone() for m, t in ops.delta_backward(*x, do, dsT=dsT, want_ds0=False).items()}
+    want = ops.delta_backward(*tail, do[:, T - n:].contiguous(), s0=mid, dsT=dsT, want_ds0=False)
+    for m in want:  # bf16 roundings of two forms of the same sums: 2^-8 each
+        assert ref.rel(got[m], want[m].cpu()) <= 2 * 2.0 ** -8, m
+    assert ops.device_status() == 0
+
+
+def test_pools_beyond_32_bits():
+    P, H = 140000, 4
+    pool = torch.empty(P, H, 64, 64, device="cuda")
+    assert pool.numel() > 1 << 31
+    x = _cu(ref.inputs(2, 1, 2, H, BF16, seed=9))
+    pool[P - 1], pool[7] = x["s0"][0], x["s0"][1]
+    ops.state_copy(pool, *(torch.tensor(i, dtype=torch.int32, device="cuda") for i in ([P - 1], [P - 2])))
+    o, _ = ops.delta_forward(*_args(x), s0=pool, slots=torch.tensor([P - 2, 7], dtype=torch.int32, device="cuda"))
+    want, sT = ops.delta_forward(*_args(x), s0=x["s0"])
+    assert torch.equal(o, want) and torch.equal(pool[P - 2], sT[0]) and torch.equal(pool[7], sT[1])
+    assert torch.equal(pool[P - 1], x["s0"][0]) and ops.device_status() == 0
