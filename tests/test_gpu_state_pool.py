@@ -91,6 +91,20 @@ def test_compact_largest_pool():
     assert torch.equal(got.cpu(), new) and index.tolist() == ri and count.item() == rn
 
 
+@pytest.mark.parametrize("shape,dim", [((0, 7, 4), 1), ((7, 0), 0), ((2, 7, 0, 64), 1), ((0, 4), 0), ((0, 0, 4), 1)])
+def test_compact_pools_without_bytes(shape, dim):
+    """No layers, empty slots or no slots: nothing moves, and the places are still told."""
+    P = shape[dim]
+    live = [i % 3 != 1 for i in range(P)]
+    pool = torch.empty(shape, device="cuda")
+    index, count = ops.state_compact(pool, torch.tensor(live, dtype=torch.bool, device="cuda"), slot_dim=dim)
+    assert index.tolist() == [sum(live[:i]) if x else -1 for i, x in enumerate(live)]
+    assert count.tolist() == [sum(live)] and ops.device_status() == 0
+    one = _i32([0])
+    ops.state_copy(pool, one, one, slot_dim=dim)
+    assert ops.device_status() == 0
+
+
 def test_copy_and_compact_replayed_in_a_graph():
     """Captured once, replayed over new indices: the calls read them from the device."""
     pool = _pool((2, 12, 512))

@@ -33,10 +33,11 @@ constexpr int kCompactStage = 32 * 1024;   // two stages, three blocks per SM
 
 // Bytes of a task's range: at most `most`, a multiple of 16, so that `blocks` blocks have the same number
 // of tasks as nearly as it can be, but no less than 512 where `most` allows (shorter bulk copies waste
-// their issue).
+// their issue).  A pool of no layers or of empty slots has no tasks, and any range serves.
 __host__ __device__ int64_t pick_range(int64_t layers, int64_t slot_bytes, int64_t most, int64_t blocks)
 {
     if (most < 16) most = 16;
+    if (layers == 0 || slot_bytes == 0) return most / 16 * 16;
     const int64_t least = most < 512 ? most : 512, per = (slot_bytes + most - 1) / most;
     const int64_t rounds = (layers * per + blocks - 1) / blocks, even = rounds * blocks / layers;
     const int64_t range = even > per ? (slot_bytes + even - 1) / even : most;
