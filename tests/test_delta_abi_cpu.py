@@ -126,6 +126,24 @@ def test_backward_nothing_to_do(lib):
     assert lib.rwkv_delta_backward_workspace_bytes(1, 8, 3, 4, 64, 1, 0, 1, ctypes.byref(b)) == -2
 
 
+@pytest.mark.parametrize("B,T,H,packed,nseq", [(1 << 21, 1, 64, 0, 0), (1 << 20, 8, 64, 0, 0), (1, 1 << 21, 64, 1, 1 << 21),
+                                               (1 << 17, 9, 64, 0, 0), (1 << 24, 1, 1, 0, 0), (1, 1 << 30, 32, 0, 0)])
+@pytest.mark.parametrize("shared", [1, 2])
+def test_backward_workspace_of_many_sequences(lib, B, T, H, packed, nseq, shared):
+    """Sizes within the limits are not refused, however many sequences they are of."""
+    Hk, n = max(H // shared, 1), nseq if packed else B
+    b = ctypes.c_size_t(1)
+    shares = 0 if Hk == H else 2 * B * T * H * 64 * 4
+    for bf16 in (0, 1):
+        assert lib.rwkv_delta_backward_workspace_bytes(B, T, Hk, H, 64, nseq, packed, bf16, ctypes.byref(b)) == 0
+        if not bf16 or (T // n if packed else T) < 9:  # token walks: a state and a gradient for every segment of 8 tokens
+            segments = T // 8 + n if packed else B * -(-T // 8)
+            states = 0 if T <= 8 and not packed else 2 * segments * H * 64 * 64 * 4
+            assert b.value == states + shares
+        else:  # chunks: T in two tiles of 8 KB, four more tiles
+            assert b.value == B * -(-T // 64) * H * 6 * 8192 + shares
+
+
 def test_state_copy_refusals(lib):
     f = lambda layers=1, nslots=8, sb=64, pool=_p(0), n=2, src=_p(1), dst=_p(2): lib.rwkv_state_copy(  # noqa: E731
         layers, nslots, sb, pool, n, src, dst)

@@ -442,9 +442,8 @@ int delta_bwd_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int6
 {
     int rc = delta_sizes(B, T, Hk, H, N, nseq, packed, 0, false, z);
     if (rc) return rc;
-    int64_t per, all;  // the largest workspace: a 64 x 64 fp32 state every 8 tokens and two fp32 shares
-    if (!mul_ok(T / 8 + z->nseq + 2, H, &per) || !mul_ok(per, B > 0 ? B : 1, &all) || !mul_ok(all, 1 << 16, &all))
-        return fail(RWKV_ERR_SHAPE, "workspace size overflows%s");
+    // No overflow here: 2^31 (chunk, head) pairs at most are 2^34 segments of 8 tokens, and neither layout
+    // takes 2^16 bytes for one.
     const wkv::DeltaArgs a = delta_shape(B, T, Hk, H, *z, packed, bf16);
     *bytes = z->nseq == 0 || z->nh == 0 || N != 64 ? 0
              : delta_chunked(T, *z, packed, bf16, kDeltaBwdChunkedTokens) ? wkv::delta_backward_tc_workspace_bytes(a)
