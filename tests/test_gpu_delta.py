@@ -117,6 +117,17 @@ def test_forward_slots(dtype, T, inplace):
         assert torch.equal(dpool.cpu(), pool)
 
 
+@pytest.mark.parametrize("T", [1, 7, 40])
+def test_forward_slots_without_a_pool(T):
+    """No state is read or kept, so no slot is past a pool either."""
+    x = _cu(ref.inputs(2, T, 1, 2, BF16, seed=T))
+    slots = torch.tensor([100, 1], dtype=torch.int32, device="cuda")
+    assert ops.device_status() == 0
+    o = ops.delta_forward(*_args(x), slots=slots, want_state=False)
+    assert ops.device_status() == 0
+    assert torch.equal(o, ops.delta_forward(*_args(x), want_state=False))
+
+
 HARD = ["no_decay", "reset", "fast", "far", "gate0", "gate1_same_key", "gate2", "zero_keys", "correlated", "growth"]
 
 

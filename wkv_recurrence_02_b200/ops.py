@@ -437,8 +437,9 @@ def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=Non
     1/sqrt(N).  offsets: int32 [sequences+1], the runs of tokens of a packed call (B = 1).
     s0: [sequences,H,N,N] fp32 or None (zero); with slots (int32 [sequences]), a pool
     [P,H,N,N] whose slot slots[i] is sequence i's state, updated in place unless another pool
-    is given as sT; a negative slot is a sequence without a state.  Returns (o, sT), or o; an o
-    allocated here is not set for tokens outside every sequence.
+    is given as sT; a negative slot is a sequence without a state.  Slots without a pool (s0 and
+    sT None, want_state False) are not looked at: every sequence starts from zero.  Returns (o, sT),
+    or o; an o allocated here is not set for tokens outside every sequence.
     """
     lib = load()
     B, T, Hk, H, N, nseq, dt = _delta_shapes(q, k, v, g, beta, offsets)
@@ -450,7 +451,9 @@ def delta_forward(q, k, v, g, beta, scale=None, s0=None, offsets=None, slots=Non
                 raise ValueError("slots need a pool: s0, sT or both")
             sT = s0
     pool = s0 if s0 is not None else sT
-    nslots = nseq if slots is None or pool is None else pool.shape[0]
+    if pool is None:  # no state to find or to keep: the slots name nothing
+        slots = None
+    nslots = nseq if slots is None else pool.shape[0]
     state = (nslots, H, N, N)
     _tensor(s0, "s0", torch.float32, state, dev)
     if o is None:
