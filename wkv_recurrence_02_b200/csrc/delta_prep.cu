@@ -298,7 +298,10 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
         }
     }
     if (__syncthreads_or(!ok)) {
-        if (tid == 0) record_status(p.status, kStatusTimeout);
+        if (tid == 0) {
+            record_status(p.status, kStatusTimeout);
+            bar_wait_spin(bar, 0, 64u * p.spin_limit);  // the copy in flight
+        }
         return;
     }
     // ---- T
