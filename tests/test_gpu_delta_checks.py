@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import delta_ref as ref
-from test_gpu_delta import BF16, F32, _args, _check_backward, _check_forward, _cu
+from test_gpu_delta import BF16, F32, SCALE, _args, _check_backward, _check_forward, _cu
 from wkv_recurrence_02_b200 import build, ops
 
 pytestmark = pytest.mark.gpu
@@ -96,6 +96,49 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_survives():
         assert status == -6
         _check_forward(x)
         _check_backward(x, BF16)
+
+
+@pytest.mark.parametrize("Hk,H,lens", [(2, 2, None), (1, 3, None), (2, 2, [70, 0, 1, 129])])
+def test_every_kernel_whose_wait_runs_out_writes_nothing(Hk, H, lens):
+    """T's kernel, both walks and the gradient kernel each: no output, nothing in the workspace but the
+    sums of the value heads' shares; the next call is as if nothing had been."""
+    lib, p = ops.load(), ops._ptr
+    T, n = (200, 1) if lens is None else (sum(lens), len(lens))
+    x = _cu(ref.inputs(1, T, Hk, H, BF16, seed=4, nseq=n))
+    off = None if lens is None else torch.tensor([sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32, device="cuda")
+    bytes_f = ops.delta_forward_workspace_bytes(1, T, Hk, H, nseq=n, packed=lens is not None)
+    bytes_b = ops.delta_backward_workspace_bytes(1, T, Hk, H, nseq=n, packed=lens is not None)
+    shares = 0 if H == Hk else 2 * T * H * 64 * 4
+
+    def run():
+        ops._use_current_stream(lib, x["q"].device)
+        ws = [torch.full((b,), 171, dtype=torch.uint8, device="cuda") for b in (bytes_f, bytes_b)]
+        out = {m: torch.full_like(x[i], 5.0) for m, i in
+               (("o", "v"), ("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"), ("dbeta", "beta"), ("sT", "s0"), ("ds0", "s0"))}
+        a = [1, T, Hk, H, 64, *[p(t) for t in _args(x)], SCALE, n, p(off)]
+        ops._check(lib.rwkv_delta_forward_bf16(*a, 0, None, p(x["s0"]), p(out["o"]), p(out["sT"]), p(ws[0]), bytes_f))
+        ops._check(lib.rwkv_delta_backward_bf16(*a, p(x["s0"]), p(x["do"]), p(x["dsT"]),
+                                                *[p(out[m]) for m in ("dq", "dk", "dv", "dg", "dbeta", "ds0")], p(ws[1]),
+                                                bytes_b))
+        return out, ws
+
+    want, _ = run()
+    assert ops.device_status() == 0
+    prev = lib.rwkv_debug_inject_timeout(1)
+    try:
+        out, ws = run()
+        status = ops.device_status()
+    finally:
+        lib.rwkv_debug_inject_timeout(prev)
+    assert status == -6
+    assert (ws[0] == 171).all() and (ws[1][:bytes_b - shares] == 171).all()
+    for m, t in out.items():
+        if H == Hk or m not in ("dq", "dk"):  # those are sums of shares, which nothing wrote
+            assert (t == 5.0).all(), m
+    again, _ = run()
+    assert ops.device_status() == 0
+    for m in want:
+        assert torch.equal(want[m], again[m]), m
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

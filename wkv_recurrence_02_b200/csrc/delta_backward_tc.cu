@@ -66,6 +66,7 @@ struct StateParams {
     unsigned char *ds, *dw;     // [chunks][H] tiles: dS after the chunk, dW
     int *status;
     uint32_t spin_limit;
+    int inject_timeout;
 };
 
 __global__ void __launch_bounds__(kThreads, 2)
@@ -93,6 +94,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
     // pass two more chunks here before the chain waits for this one
     const uint32_t bar_s0 = smem_u32(&bars[19]);
     const uint32_t bar_drain = smem_u32(&bars[22]);
+    const uint32_t bar_never = smem_u32(&bars[23]);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, see elect_one
@@ -107,8 +109,8 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
     const int64_t ntok = p.B * p.T;
 
     if (tid == 0) {
-        for (int i = 0; i < 23; ++i)
-            bar_init(smem_u32(&bars[i]), i == 11 || i == 12 ? 128 : i == 22 ? 2 : i >= 19 ? 64 : 1);
+        for (int i = 0; i < 24; ++i)
+            bar_init(smem_u32(&bars[i]), i == 11 || i == 12 ? 128 : i == 22 ? 2 : i >= 19 && i < 22 ? 64 : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         misc[1] = 0;
     }
@@ -149,7 +151,34 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             __syncwarp();
         }
     }
-    int ok = 1, abort = 0;
+    // Drain after a wait that ran out, then release tensor memory.
+    auto leave = [&] {
+        fence_before();
+        const int abort = __syncthreads_or(misc[1] != 0);
+        fence_after();
+        if (abort) {
+            record_status(p.status, kStatusTimeout);
+            if ((warp == 0 || warp == 4) && elect_one()) mma_commit(bar_drain);  // the two issuers
+            if (tid == 0) {
+                bar_wait(bar_drain, 0, p.spin_limit);
+                for (int i = 0; i < 7; ++i)  // copies in flight: a barrier that nothing will complete runs out
+                    for (uint32_t ph = 0; ph < 2; ++ph) bar_wait(smem_u32(&bars[i]), ph, 200);
+            }
+        }
+        fence_before();
+        __syncthreads();
+        fence_after();
+        if (warp == 0)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols));
+        // This kernel runs beside the walk launched before it (see the launch); what follows needs both.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
+    if (p.inject_timeout) {
+        if (tid == 0 && !bar_wait(bar_never, 0, p.spin_limit)) misc[1] = 1;
+        leave();
+        return;
+    }
+    int ok = 1;
     if (warp < 4) {
         // ------------------------------------------------------------------ side group
         const int w = warp;
@@ -206,7 +235,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 scan(0);
             }
         }
-        for (int n = 0; n < nchunks && !abort; ++n) {
+        for (int n = 0; n < nchunks; ++n) {
             group_sync<1, 128>();  // the chunk's decays are there
             if (ok) ok = bar_wait(bar_a, n & 1, spin);
             fence_after();
@@ -420,7 +449,6 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             if (!ok) misc[1] = 1;  // and its waits pass from here on, in this thread and soon in all
         }
         if (warp == 5 && lane == 0) bulk_wait_all();
-        if (abort) ok = 0;
         if (ok && p.ds0 && in_bounds(p.status, sat, 32, nstate)) {
             float4 *dst = reinterpret_cast<float4 *>(p.ds0 + sat);
 #pragma unroll
@@ -428,27 +456,7 @@ delta_bwd_state_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         }
     }
     if (!ok) misc[1] = 1;
-
-    // ---- drain after an abort, then release tensor memory
-    fence_before();
-    abort = __syncthreads_or(abort || misc[1] != 0);
-    fence_after();
-    if (abort) {
-        record_status(p.status, kStatusTimeout);
-        if ((warp == 0 || warp == 4) && elect_one()) mma_commit(bar_drain);  // the two issuers
-        if (tid == 0) {
-            bar_wait(bar_drain, 0, p.spin_limit);
-            for (int i = 0; i < 7; ++i)  // copies in flight: a barrier that nothing will complete runs out
-                for (uint32_t ph = 0; ph < 2; ++ph) bar_wait(smem_u32(&bars[i]), ph, 200);
-        }
-    }
-    fence_before();
-    __syncthreads();
-    fence_after();
-    if (warp == 0)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols));
-    // This kernel runs beside the walk launched before it (see the launch); what follows needs both.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    leave();
 }
 
 // ----------------------------------------------------------------------- gradients of a chunk
@@ -495,6 +503,7 @@ struct GradParams {
     float *dq_h, *dk_h;  // [B,T,H,64] shares of the value heads, or null
     int *status;
     uint32_t spin_limit;
+    int inject_timeout;
 };
 
 // A thread's 16 columns, as pairs: [4 b + i] of block b (b = 0, 1).
@@ -676,6 +685,24 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         *reinterpret_cast<uint4 *>(sm + tile + sw[1]) = pack_block(x, 1);
     };
 
+    auto leave = [&](bool out) {  // out: a wait of this thread's ran out
+        if (warp == 7 && elect_one()) bulk_wait_all();
+        fence_before();
+        const int bad = __syncthreads_or(out);
+        fence_after();
+        if (bad && tid == 0) {
+            record_status(p.status, kStatusTimeout);
+            for (int i = 0; i < 3; ++i)  // what is in flight
+                for (uint32_t ph = 0; ph < 2; ++ph) bar_wait(bar0 + 8 * i, ph, 200);
+        }
+        __syncthreads();
+        if (warp == 0)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(256u));
+    };
+    if (p.inject_timeout) {  // there are no products yet whose end bar1 could tell
+        leave(tid == 0 && !bar_wait(bar1, 0, p.spin_limit));
+        return;
+    }
     int ok = 1;
     for (int it = 0; n < total; ++it, cur = nxt) {
         const int buf = it & 1, ph = it & 1, tQ = GO_Q + kTile * buf, tK = GO_K + kTile * buf, tW = GO_DW + kTile * buf;
@@ -949,18 +976,7 @@ delta_bwd_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         }
         n = n2;
     }
-    if (warp == 7 && elect_one()) bulk_wait_all();
-    fence_before();
-    const int bad = __syncthreads_or(!ok);
-    fence_after();
-    if (bad && tid == 0) {
-        record_status(p.status, kStatusTimeout);
-        for (int i = 0; i < 3; ++i)  // what is in flight
-            for (uint32_t ph = 0; ph < 2; ++ph) bar_wait(bar0 + 8 * i, ph, 200);
-    }
-    __syncthreads();
-    if (warp == 0)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(256u));
+    leave(!ok);
 }
 
 // Byte layout of the workspace: T, four tiles for every chunk and value head, the value heads'
@@ -1010,7 +1026,8 @@ cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(f.g), *beta = static_cast<const __nv_bfloat16 *>(f.beta);
     const StateParams sp{f.B, f.T, f.Hk, f.H, f.nseq, f.offsets, g, beta, ws + l.t, chunks, f.scale, a.dsT, a.ds0,
-                         ws + l.ds, ws + l.dw, f.status, 100000u};
+                         ws + l.ds, ws + l.dw, f.status, g_chunked_inject_timeout ? 100u : 100000u,
+                         g_chunked_inject_timeout};
     // The two walks read T and the inputs and nothing of each other: this one may start while the
     // first still runs (a programmatic launch; T's kernel was complete before the first began).  It
     // ends only after the first has, so that the next kernel, launched as usual, follows both.
@@ -1035,7 +1052,8 @@ cudaError_t delta_backward_tc_launch(const DeltaBwdArgs &a, cudaStream_t s)
                         ws + l.states, ws + l.us, ws + l.ds, ws + l.dw, chunks,
                         static_cast<__nv_bfloat16 *>(a.dq), static_cast<__nv_bfloat16 *>(a.dk),
                         static_cast<__nv_bfloat16 *>(a.dv), static_cast<__nv_bfloat16 *>(a.dg),
-                        static_cast<__nv_bfloat16 *>(a.dbeta), dq_h, dk_h, f.status, 100000u};
+                        static_cast<__nv_bfloat16 *>(a.dbeta), dq_h, dk_h, f.status,
+                        g_chunked_inject_timeout ? 100u : 100000u, g_chunked_inject_timeout};
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         sms <= 0)

@@ -52,6 +52,7 @@ struct Params {
     int64_t nchunks;        // chunks of the call, the most there can be
     int *status;
     uint32_t spin_limit;
+    int inject_timeout;
 };
 
 // One 16 x 16 operand in two bf16 terms.  As A (and as the accumulators of two n = 8 products lie):
@@ -154,6 +155,13 @@ delta_prep_kernel(const __grid_constant__ CUtensorMap map_k, const Params p)
     const int64_t t0 = first + static_cast<int64_t>(c) * kC, ntok = p.B * p.T;
     const int tv = static_cast<int>(len - (t0 - first) < kC ? len - (t0 - first) : kC);
     const uint32_t bar = smem_u32(sm + OFF_BAR);
+    if (p.inject_timeout) {  // no copy is started that the barrier could tell of
+        if (tid == 0) {
+            bar_init(bar, 1);
+            if (!bar_wait(bar, 0, p.spin_limit)) record_status(p.status, kStatusTimeout);
+        }
+        return;
+    }
     if (tid == 0) {
         bar_init(bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -375,7 +383,7 @@ cudaError_t delta_prep_launch(const DeltaArgs &a, void *t_out, cudaStream_t s)
     if (!make_map(&mk, a.k, a.B, a.T, a.Hk)) return cudaErrorInvalidValue;
     const Params p{a.B, a.T, a.Hk, a.H, a.nseq, a.offsets, static_cast<const __nv_bfloat16 *>(a.g),
                    static_cast<const __nv_bfloat16 *>(a.beta), static_cast<unsigned char *>(t_out), chunks, a.status,
-                   100000u};
+                   g_chunked_inject_timeout ? 100u : 100000u, g_chunked_inject_timeout};
     delta_prep_kernel<<<static_cast<unsigned>(chunks * a.H), kThreads, kSmemBytes, s>>>(mk, p);
     return cudaGetLastError();
 }
