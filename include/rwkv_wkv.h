@@ -401,10 +401,11 @@ int rwkv_wkv6_forward_bf16_noalloc(int64_t B, int64_t T, int64_t H, int64_t N,
                                    uint16_t *y, float *sT, int segments);
 
 /* Test hook for the failure path (process-wide).  While enabled, every chunked WKV-6 forward
- * kernel and every kernel of the chunked delta rule (forward and backward) first waits on a
- * barrier that nothing signals, with a short bound; the wait runs out, the kernel records RWKV_ERR_TIMEOUT in the device status word, releases its
- * resources and returns without computing (outputs are then unspecified).  No fault or
- * hang is involved.  Returns the previous setting. */
+ * kernel, every kernel of the chunked delta rule (forward and backward) and both kernels of
+ * the state pools wait, before they compute or move anything, on a barrier that nothing
+ * signals, with a short bound; the wait runs out, the kernel records RWKV_ERR_TIMEOUT in the
+ * device status word, releases its resources and returns (outputs are then unspecified).  No
+ * fault or hang is involved.  Returns the previous setting. */
 int rwkv_debug_inject_timeout(int enable);
 
 /* ------------------------------------------------------------------ runtime plumbing */

@@ -128,6 +128,30 @@ def test_copy_and_compact_replayed_in_a_graph():
         assert torch.equal(got.cpu(), want) and index.tolist() == ri and count.item() == rn
 
 
+@pytest.mark.parametrize("shape,dim", [((3, 40, 5, 64), 1), ((6, 12004), 0), ((200, 2, 64, 64), 0)])
+def test_a_wait_that_runs_out_moves_nothing(shape, dim):
+    lib = ops.load()
+    pool, P = _pool(shape), shape[dim]
+    got = pool.cuda()
+    src, dst = list(range(P)), [(i + 1) % P for i in range(P)]
+    live = torch.arange(P) % 3 != 0
+    assert ops.device_status() == 0
+    prev = lib.rwkv_debug_inject_timeout(1)
+    try:
+        for call in (lambda: ops.state_copy(got, _i32(src), _i32(dst), slot_dim=dim),
+                     lambda: ops.state_compact(got, live.cuda(), slot_dim=dim)):
+            call()
+            assert ops.device_status() == -6
+            assert torch.equal(got.cpu(), pool)
+    finally:
+        lib.rwkv_debug_inject_timeout(prev)
+    _copy(pool, src, dst, dim)
+    index, count = ops.state_compact(got, live.cuda(), slot_dim=dim)
+    new, ri, rn = ref.compacted(pool, live.tolist(), dim)
+    assert torch.equal(got.cpu(), new) and index.tolist() == ri and count.tolist() == [rn]
+    assert ops.device_status() == 0
+
+
 def test_binding_refusals():
     pool = _pool((4, 8)).cuda()
     with pytest.raises(TypeError):

@@ -26,7 +26,6 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 256;
-constexpr uint32_t kWaitLimit = 100000;
 constexpr int kCopySmem = 224 * 1024;      // the copy kernel's block owns an SM
 constexpr int kZeroBytes = 8 * 1024;       // zeros for freed slots, and the largest copy range
 constexpr int kCompactStage = 32 * 1024;   // two stages, three blocks per SM
@@ -48,7 +47,22 @@ __host__ __device__ int64_t pick_range(int64_t layers, int64_t slot_bytes, int64
 struct CopyParams {
     StateCopyArgs a;
     int stage;              // bytes of one of the two stages
+    uint32_t wait_limit;
+    int inject_timeout;
 };
+
+// Whether the warp's wait for its it-th stage was met.  If it ran out, the copies in flight (the next
+// stage's too, with `next`) have been waited for as well, with the same limit.
+template <typename P> __device__ __forceinline__ bool arrived(const P &p, const uint64_t *bars, int64_t it, bool next)
+{
+    const uint32_t bar = smem_u32(&bars[it & 1]), phase = static_cast<uint32_t>((it >> 1) & 1);
+    const bool ok = p.inject_timeout ? bar_wait(smem_u32(&bars[2]), 0, p.wait_limit) : bar_wait(bar, phase, p.wait_limit);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((threadIdx.x & 31) == 0) record_status(p.a.status, kStatusTimeout);
+    bar_wait(bar, phase, p.wait_limit);
+    if (next) bar_wait(smem_u32(&bars[(it + 1) & 1]), static_cast<uint32_t>(((it + 1) >> 1) & 1), p.wait_limit);
+    return false;
+}
 
 // Shared memory: the two stages, zeros, then per pair its source and destination, the pair that
 // loads its source (itself, an earlier one, -1: zeros, -2: the pair does nothing) and, for a
@@ -59,7 +73,7 @@ state_copy_kernel(const CopyParams p)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     unsigned char *zeros = sm + 2 * p.stage;
-    __shared__ uint64_t bars[2];
+    __shared__ uint64_t bars[3];  // the stages loaded; the third is never signalled
     __shared__ int nload;
     const int n = static_cast<int>(p.a.n), tid = threadIdx.x;
     int *src = reinterpret_cast<int *>(zeros + kZeroBytes), *dst = src + n, *from = dst + n, *pos = from + n;
@@ -77,8 +91,7 @@ state_copy_kernel(const CopyParams p)
     for (int i = tid; i < kZeroBytes / 16; i += kThreads) reinterpret_cast<uint4 *>(zeros)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) {
         nload = 0;
-        bar_init(smem_u32(&bars[0]), 1);
-        bar_init(smem_u32(&bars[1]), 1);
+        for (int i = 0; i < 3; ++i) bar_init(smem_u32(&bars[i]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -135,7 +148,6 @@ state_copy_kernel(const CopyParams p)
             }
     };
     int64_t it = 0;
-    bool ok = true;
     if (blockIdx.x < tasks) load(blockIdx.x, 0);
     for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x, ++it) {
         const int st = static_cast<int>(it & 1);
@@ -144,12 +156,7 @@ state_copy_kernel(const CopyParams p)
             __syncwarp();
             load(task + gridDim.x, st ^ 1);
         }
-        ok = bar_wait(smem_u32(&bars[st]), static_cast<uint32_t>((it >> 1) & 1), kWaitLimit);
-        if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) record_status(p.a.status, kStatusTimeout);
-            bar_wait(smem_u32(&bars[st ^ 1]), static_cast<uint32_t>(((it + 1) >> 1) & 1), kWaitLimit);  // the copies in flight
-            break;
-        }
+        if (!arrived(p, bars, it, task + gridDim.x < tasks)) break;
         const int64_t layer = task / per_layer, off = task % per_layer * range;
         const uint32_t w = static_cast<uint32_t>(min(range, p.a.slot_bytes - off));
         for (int i = lane; i < n; i += 32) {
@@ -168,6 +175,8 @@ struct CompactParams {
     StateCompactArgs a;
     int64_t range, per_layer;
     int batch;              // moves per stage
+    uint32_t wait_limit;
+    int inject_timeout;
 };
 
 __global__ void __launch_bounds__(kThreads)
@@ -176,13 +185,12 @@ state_compact_kernel(const CompactParams p)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
     uint16_t *list = reinterpret_cast<uint16_t *>(sm + 2 * kCompactStage);  // live slots in order
-    __shared__ uint64_t bars[2];
+    __shared__ uint64_t bars[3];  // as above
     __shared__ int warp_sum[kThreads / 32], s_first;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nslots = static_cast<int>(p.a.nslots);
     if (tid == 0) {
         s_first = nslots;
-        bar_init(smem_u32(&bars[0]), 1);
-        bar_init(smem_u32(&bars[1]), 1);
+        for (int i = 0; i < 3; ++i) bar_init(smem_u32(&bars[i]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     int count = 0;
@@ -244,12 +252,7 @@ state_compact_kernel(const CompactParams p)
             __syncwarp();
             load(it + 1);
         }
-        const bool ok = bar_wait(smem_u32(&bars[st]), static_cast<uint32_t>((it >> 1) & 1), kWaitLimit);
-        if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) record_status(p.a.status, kStatusTimeout);
-            bar_wait(smem_u32(&bars[st ^ 1]), static_cast<uint32_t>(((it + 1) >> 1) & 1), kWaitLimit);  // the copies in flight
-            break;
-        }
+        if (!arrived(p, bars, it, it + 1 < total)) break;
         int64_t base;
         uint32_t w;
         int m0, m1;
@@ -263,6 +266,8 @@ state_compact_kernel(const CompactParams p)
     }
     bulk_wait_all();
 }
+
+uint32_t wait_limit() { return g_chunked_inject_timeout ? 100u : 100000u; }
 
 int64_t sms()
 {
@@ -280,7 +285,7 @@ cudaError_t state_copy_launch(const StateCopyArgs &a, cudaStream_t s)
     const cudaError_t e = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCopySmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(std::min(a.layers * ((a.slot_bytes + 511) / 512), sms()));
-    state_copy_kernel<<<grid, kThreads, kCopySmem, s>>>(CopyParams{a, static_cast<int>(stage)});
+    state_copy_kernel<<<grid, kThreads, kCopySmem, s>>>(CopyParams{a, static_cast<int>(stage), wait_limit(), g_chunked_inject_timeout});
     return cudaGetLastError();
 }
 
@@ -294,7 +299,8 @@ cudaError_t state_compact_launch(const StateCompactArgs &a, cudaStream_t s)
                                                2 * kCompactStage + static_cast<int>(kMaxCompactSlots) * 2 + 128);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(std::min(std::max<int64_t>(a.layers * per_layer, 1), blocks));
-    state_compact_kernel<<<grid, kThreads, smem, s>>>(CompactParams{a, range, per_layer, static_cast<int>(kCompactStage / range)});
+    state_compact_kernel<<<grid, kThreads, smem, s>>>(CompactParams{a, range, per_layer, static_cast<int>(kCompactStage / range),
+                                                                  wait_limit(), g_chunked_inject_timeout});
     return cudaGetLastError();
 }
 
