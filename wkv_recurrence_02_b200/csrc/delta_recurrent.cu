@@ -160,8 +160,8 @@ delta_recurrent_kernel(int64_t B, int64_t Tn, int64_t Hk, int64_t H, int64_t nse
 // there are few heads), the rows in pairs, so that the products are two-wide instructions
 // (fma.rn.f32x2) and a sum over rows has two rounds of shuffles: 64 fma2 and 10 shuffles a token
 // where the layout above has 128 fma and 27.  Inputs come through shared memory (cp.async), kGroups - 1 groups of kGroup tokens
-// ahead, a ring to each warp: no barrier.  Measured, one sequence of 4 heads, 256 tokens fp32: 56 us
-// (0.2 us a token: one warp on each scheduler, a third of its cycles issue), against 127 with the
+// ahead, a ring to each warp: no barrier.  Measured, one sequence of 4 heads, 256 tokens fp32: 61 us
+// a call (0.23 us a token: one warp on each scheduler, a third of its cycles issue), against 127 with the
 // kernel above (one token ahead, a miss's latency each).
 constexpr int kGroup = 4, kGroups = 4, kRing = kGroup * kGroups;
 template <int COLS> constexpr int kRow = 2 * kN + 8 * COLS;  // a token in the ring: q, k, the warp's columns of v
